@@ -1,0 +1,340 @@
+"""GPU parity of jf_sample and jf_accept_sampled against the float64 oracle: tokens and paths exactly, log-probabilities
+to float32 rounding."""
+import numpy as np
+import pytest
+import torch
+
+from oracle.sampling import accept_sampled as oracle_accept, sample_row
+from tree_verify_attention_jf_b200 import _lib, api
+
+pytestmark = pytest.mark.gpu
+
+# One rounding to float32 of the log-probability (half a step, 2^-24 relative), of which the oracle's own float64
+# sums take nothing visible; 2^-23 with an absolute floor for log-probabilities near 0, where ln(1 - tiny) carries the
+# float64 rounding of a sum of up to 2^19 terms (2^19 * 2^-53 = 2^-34).
+LP_REL, LP_ABS = 2.0 ** -23, 2.0 ** -33
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a))
+    return (t if dtype is None else t.to(dtype)).cuda()
+
+
+def make_rows(seed, R, V, sigma=2.0, plant=8):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((R, V), dtype=np.float32) * np.float32(sigma)
+    for r in range(R):
+        n = min(plant, V)
+        x[r, rng.choice(V, n, replace=False)] = x[r].max() + rng.uniform(0, 5) - np.log(np.arange(1, n + 1))
+    return x.astype(np.float32), rng
+
+
+def params(rng, R, kind):
+    f = lambda a: np.asarray(a, np.float32)
+    t, k, p, m = f(rng.uniform(0.4, 1.4, R)), np.zeros(R, np.int32), np.ones(R, np.float32), np.zeros(R, np.float32)
+    if kind in ("top_k", "all"):
+        k = rng.integers(1, 60, R).astype(np.int32)
+    if kind in ("top_p", "all"):
+        p = f(rng.uniform(0.3, 0.995, R))
+    if kind in ("min_p", "all"):
+        m = f(rng.uniform(0.001, 0.3, R))
+    if kind == "mixed":
+        t[rng.random(R) < 0.2] = 0
+        k = np.where(rng.random(R) < 0.5, rng.integers(1, 3000, R), 0).astype(np.int32)
+        p = np.where(rng.random(R) < 0.5, f(rng.uniform(0, 1, R)), np.float32(1)).astype(np.float32)
+        m = np.where(rng.random(R) < 0.4, f(rng.uniform(0, 1, R)), np.float32(0)).astype(np.float32)
+    return t, k, p, m
+
+
+def run(x, u, par, dtype=torch.float32, pad=0, **kw):
+    """x float32 rows (bf16-representable for bf16); returns numpy (token, logprob)."""
+    R, V = x.shape
+    big = torch.full((R, V + pad), float("nan"), dtype=dtype, device="cuda")
+    big[:, :V] = dev(x, dtype)
+    got = api.sample(big[:, :V], dev(u), *(dev(a) for a in par), **kw)
+    torch.cuda.synchronize()
+    return got["token"].cpu().numpy(), got["logprob"].cpu().numpy()
+
+
+def check(x, u, par, got):
+    tok, lp = got
+    for r in range(x.shape[0]):
+        want, wlp = sample_row(x[r], float(u[r]), *(float(par[0][r]), int(par[1][r]), float(par[2][r]), float(par[3][r])))
+        assert tok[r] == want, (r, tok[r], want, [a[r] for a in par], u[r])
+        if np.isinf(wlp):
+            assert lp[r] == wlp
+        else:
+            assert abs(lp[r] - wlp) <= LP_REL * abs(wlp) + LP_ABS, (r, lp[r], wlp)
+
+
+def bf16(x):
+    return torch.from_numpy(x).to(torch.bfloat16).float().numpy()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,V", [(3, 1), (5, 2), (4, 7), (33, 31), (17, 1000), (9, 4099), (20, 32003), (6, 151936)])
+@pytest.mark.parametrize("kind", ["none", "top_k", "top_p", "min_p", "all", "mixed"])
+def test_matches_oracle(dtype, R, V, kind):
+    x, rng = make_rows(1000 + V, R, V)
+    if dtype == torch.bfloat16:
+        x = bf16(x)  # coarse values: many equal logits, ordered by id
+    par, u = params(rng, R, kind), rng.random(R, dtype=np.float32)
+    u[0] = 0.0
+    u[-1] = np.float32(1 - 2.0 ** -24)
+    check(x, u, par, run(x, u, par, dtype, pad=(V * 5) % 13))
+
+
+def test_largest_vocabulary():
+    V = 524288
+    x, rng = make_rows(7, 3, V)
+    par, u = params(rng, 3, "all"), rng.random(3, dtype=np.float32)
+    check(x, u, par, run(x, u, par))
+    par = params(rng, 3, "top_p")
+    check(x, u, par, run(x, u, par))
+
+
+@pytest.mark.parametrize("V", [50, 5000, 151936])
+def test_equal_logits_are_taken_in_id_order(V):
+    # a uniform row: every sum is exact on both sides
+    x = np.full((8, V), -7.25, np.float32)
+    u = np.array([0, 1 / 16, 0.25, 0.5, 0.75, 0.875, 15 / 16, 1 - 2.0 ** -24], np.float32)
+    one = np.ones(8, np.float32)
+    for k, p, m in ((0, 1, 0), (17, 1, 0), (0, 0.5, 0), (40, 0.25, 1), (V, 1, 1), (0, 0, 0)):
+        par = (one * np.float32(0.7), np.full(8, k, np.int32), np.full(8, p, np.float32), np.full(8, m, np.float32))
+        check(x, u, par, run(x, u, par))
+
+
+@pytest.mark.parametrize("levels", [2, 3, 40])
+def test_few_distinct_values(levels):
+    # heavy ties across the cut, both signs and both zeros
+    rng = np.random.default_rng(levels)
+    vals = np.concatenate([[0.0, -0.0], np.linspace(-1, 1, max(0, levels - 1))]).astype(np.float32)
+    x = vals[rng.integers(0, len(vals), (24, 20011))]
+    par = params(rng, 24, "mixed")
+    u = rng.random(24, dtype=np.float32)
+    check(x, u, par, run(x, u, par))
+    check(bf16(x), u, par, run(bf16(x), u, par, torch.bfloat16, pad=3))
+
+
+def test_masked_infinite_and_nan_logits():
+    V = 3001
+    x, rng = make_rows(3, 12, V)
+    inf = np.float32(np.inf)
+    x[0] = -inf                                  # nothing left
+    x[1] = np.nan
+    x[2] = -inf
+    x[2, 1234] = -5                              # one token left
+    x[3, rng.random(V) < 0.9] = -inf
+    x[4, rng.random(V) < 0.5] = np.nan
+    x[5, [10, 2000]] = inf                       # +inf shares the weight
+    x[6] = np.finfo(np.float32).min              # a mask of the type's lowest value over the whole row
+    x[7, rng.random(V) < 0.9] = np.finfo(np.float32).min
+    x[8] = -inf
+    x[8, 7] = np.finfo(np.float32).min
+    x[9, 5] = np.finfo(np.float32).max
+    x[10, :] = 0
+    x[10, 100] = -inf
+    x[11, 0] = np.nan
+    for kind in ("none", "all", "top_p", "mixed"):
+        par, u = params(rng, 12, kind), rng.random(12, dtype=np.float32)
+        check(x, u, par, run(x, u, par))
+
+
+def test_temperatures_from_tiny_to_huge():
+    x, rng = make_rows(4, 8, 9001)
+    t = np.array([1e-38, 1e-6, 1e-2, 0.1, 1.0, 10.0, 1e4, 1e38], np.float32)
+    u = rng.random(8, dtype=np.float32)
+    for k, p, m in ((0, 1, 0), (500, 1, 0), (0, 0.9, 0), (0, 1, 0.5), (100, 0.7, 0.01)):
+        par = (t, np.full(8, k, np.int32), np.full(8, p, np.float32), np.full(8, m, np.float32))
+        check(x, u, par, run(x, u, par))
+
+
+def test_parameters_left_out_are_off():
+    x, rng = make_rows(5, 4, 700)
+    t, u = rng.uniform(0.5, 1, 4).astype(np.float32), rng.random(4, dtype=np.float32)
+    off = (t, np.zeros(4, np.int32), np.ones(4, np.float32), np.zeros(4, np.float32))
+    got = api.sample(dev(x), dev(u), dev(t))
+    check(x, u, off, (got["token"].cpu().numpy(), got["logprob"].cpu().numpy()))
+    only = api.sample(dev(x), dev(u), dev(t), out=dict(token=got["token"].clone().fill_(-9)))
+    assert torch.equal(only["token"], got["token"]) and "logprob" not in only
+
+
+def test_bad_parameters_leave_their_row_unwritten():
+    x, rng = make_rows(6, 12, 500)
+    par, u = params(rng, 12, "all"), rng.random(12, dtype=np.float32)
+    t, k, p, m = (a.copy() for a in par)
+    t[0], t[1], t[2], k[3], p[4], p[5], m[6], m[7], u[8], u[9], u[10] = (
+        -1, np.nan, np.inf, -1, -0.1, 1.1, np.nan, 1.5, 1.0, -0.1, np.nan)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = dict(token=torch.full((12,), -77, dtype=torch.int32, device="cuda"), logprob=torch.full((12,), 5.0, device="cuda"))
+    tok, lp = run(x, u, (t, k, p, m), out=out, dev_status=st)
+    assert int(st.item()) == _lib.JF_ERR_DEVICE_CHECK
+    assert (tok[:11] == -77).all() and (lp[:11] == 5.0).all()
+    check(x[11:], u[11:], [a[11:] for a in (t, k, p, m)], (tok[11:], lp[11:]))
+
+
+def test_repeats_graph_replays_and_streams_agree_bit_for_bit():
+    x, rng = make_rows(8, 40, 50021)
+    par, u = params(rng, 40, "mixed"), rng.random(40, dtype=np.float32)
+    d = [dev(x), dev(u)] + [dev(a) for a in par]
+    ref = api.sample(*d)
+    torch.cuda.synchronize()
+    out = {k: torch.empty_like(v) for k, v in ref.items()}
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+        api.sample(*d, out=out)
+    for _ in range(3):
+        for v in out.values():
+            v.fill_(-5)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[k], ref[k]) for k in ref)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    ra = [api.sample(*d, stream=a) for _ in range(4)]
+    rb = [api.sample(*d, stream=b) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(r[k], ref[k]) for r in ra + rb for k in ref)
+
+
+def test_refusals():
+    x, u, t = torch.zeros(2, 8, device="cuda"), torch.zeros(2, device="cuda"), torch.ones(2, device="cuda")
+    with pytest.raises(TypeError):
+        api.sample(x.half(), u, t)
+    with pytest.raises(TypeError):
+        api.sample(x, u.double(), t)
+    with pytest.raises(ValueError):
+        api.sample(x[0], u, t)
+    with pytest.raises(ValueError):
+        api.sample(x.t(), u, t)
+    with pytest.raises(ValueError):
+        api.sample(x, u[:1], t)
+    with pytest.raises(ValueError):
+        api.sample(x, u, t, top_k=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        api.sample(x, u.cpu(), t)
+    with pytest.raises(_lib.JFError):
+        api.sample(x[:, 1:], u, t)  # not 16-byte aligned
+    with pytest.raises(_lib.JFError):
+        api.sample(x[:1].expand(2, 8), u, t)  # rows on top of each other
+    assert api.sample(x[:0], u[:0], t[:0])["token"].shape == (0,)
+
+
+# ---------------------------------------------------------------------------------------------- the walk
+def walk_case(seed, B, N, V, D, lift=4.0, sigma=2.0):
+    rng = np.random.default_rng(seed)
+    parent = np.array([[-1] + [int(rng.integers(max(0, i - 6), i)) for i in range(1, N)] for _ in range(B)], np.int32)
+    token = rng.integers(0, V, (B, N)).astype(np.int32)
+    x = rng.standard_normal((B, N, V), dtype=np.float32) * np.float32(sigma)
+    for b in range(B):
+        for i in range(1, N):  # every child's token stands out at its parent
+            row = x[b, parent[b, i]]
+            row[token[b, i]] = row.max() + rng.uniform(0, lift)
+    return token, parent, x, rng.random((B, D + 1), dtype=np.float32), rng
+
+
+def check_walk(case, par, D, got):
+    token, parent, x, u = case[:4]
+    acc, path, bonus, lp = oracle_accept(token, parent, x, u, D, *par)
+    assert np.array_equal(got["accepted_len"].cpu().numpy(), acc)
+    assert np.array_equal(got["path"].cpu().numpy(), path)
+    assert np.array_equal(got["bonus"].cpu().numpy(), bonus)
+    g = got["logprob"].cpu().numpy()
+    fin = np.isfinite(lp)
+    assert np.array_equal(g[~fin], lp[~fin])
+    assert (np.abs(g[fin] - lp[fin]) <= LP_REL * np.abs(lp[fin]) + LP_ABS).all()
+    return acc
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,N,V,D", [(1, 1, 5, 0), (1, 1, 40, 3), (4, 12, 9, 6), (3, 200, 4001, 16), (2, 1024, 301, 20),
+                                     (2, 40, 151936, 12), (150, 5, 333, 4)])
+@pytest.mark.parametrize("kind", ["none", "mixed"])
+def test_walk_matches_oracle(dtype, B, N, V, D, kind):
+    case = walk_case(31 * V + N, B, N, V, D)
+    if dtype == torch.bfloat16:
+        case = case[:2] + (bf16(case[2]),) + case[3:]
+    par = params(case[4], B, kind)
+    got = api.accept_sampled(dev(case[0]), dev(case[1]), dev(case[2], dtype), dev(case[3]), dev(par[0]), D,
+                             *(dev(a) for a in par[1:]))
+    acc = check_walk(case, par, D, got)
+    if N >= 12 and B > 1:
+        assert acc.max() > 0  # the case is no test of walks that end at the root only
+
+
+def test_walk_with_temperature_zero_is_jf_accept():
+    token, parent, x, u, rng = walk_case(5, 6, 64, 3000, 10)
+    t = torch.zeros(6, device="cuda")
+    got = api.accept_sampled(dev(token), dev(parent), dev(x), dev(u), t, 10)
+    ref = api.accept(dev(token), dev(parent), dev(x), 10)
+    for k in ref:
+        assert torch.equal(got[k], ref[k]), k
+
+
+def test_walk_stops_at_a_row_without_candidates():
+    token, parent, x, u, rng = walk_case(6, 3, 20, 100, 8)
+    x[1, 0] = -np.inf
+    par = params(rng, 3, "none")
+    got = api.accept_sampled(dev(token), dev(parent), dev(x), dev(u), dev(par[0]), 8)
+    check_walk((token, parent, x, u), par, 8, got)
+    assert int(got["bonus"][1]) == -1 and int(got["accepted_len"][1]) == 0
+
+
+def test_walk_device_checks_leave_the_sequence_unwritten():
+    token, parent, x, u, rng = walk_case(8, 5, 20, 100, 8)
+    par = params(rng, 5, "none")
+    par[0][1] = -2                     # temperature
+    parent[2, 4] = 4                   # parent not before its node
+    u[3, 0] = 1.0                      # the first random number
+    u[4, 8] = np.nan                   # one that the walk does not come to (checked below)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = dict(accepted_len=torch.full((5,), -9, dtype=torch.int32, device="cuda"),
+               path=torch.full((5, 9), -9, dtype=torch.int32, device="cuda"),
+               bonus=torch.full((5,), -9, dtype=torch.int32, device="cuda"),
+               logprob=torch.full((5, 9), 3.0, device="cuda"))
+    api.accept_sampled(dev(token), dev(parent), dev(x), dev(u), dev(par[0]), 8, out=out, dev_status=st)
+    assert int(st.item()) == _lib.JF_ERR_DEVICE_CHECK
+    for b in (1, 2, 3):
+        assert int(out["accepted_len"][b]) == -9 and int(out["bonus"][b]) == -9
+        assert (out["path"][b] == -9).all() and (out["logprob"][b] == 3.0).all()
+    for b in (0, 4):
+        one = [a[b:b + 1] for a in (token, parent, x, u)]
+        ref = oracle_accept(*one, 8, par[0][b:b + 1])
+        assert ref[0][0] < 8
+        assert int(out["accepted_len"][b]) == ref[0][0] and out["path"][b].cpu().tolist() == ref[1][0].tolist()
+
+
+def test_walk_replays_in_a_cuda_graph():
+    token, parent, x, u, rng = walk_case(9, 4, 64, 20000, 10)
+    par = params(rng, 4, "all")
+    d = [dev(a) for a in (token, parent, x, u)]
+    p = [dev(a) for a in par]
+    out = dict(accepted_len=torch.empty(4, dtype=torch.int32, device="cuda"),
+               path=torch.empty(4, 11, dtype=torch.int32, device="cuda"),
+               bonus=torch.empty(4, dtype=torch.int32, device="cuda"), logprob=torch.empty(4, 11, device="cuda"))
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+        api.accept_sampled(*d, p[0], 10, *p[1:], out=out)
+    for seed in (1, 2):  # new random numbers between the replays
+        case = (token, parent, x, np.random.default_rng(seed).random((4, 11), dtype=np.float32))
+        d[3].copy_(dev(case[3]))
+        g.replay()
+        torch.cuda.synchronize()
+        check_walk(case, par, 10, out)
+
+
+def test_walk_refusals():
+    z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt, device="cuda")
+    tok, par, x, u, t = z(2, 4, dt=torch.int32), z(2, 4, dt=torch.int32), z(2, 4, 8), z(2, 3), z(2)
+    with pytest.raises(TypeError):
+        api.accept_sampled(tok, par, x.double(), u, t, 2)
+    with pytest.raises(ValueError):
+        api.accept_sampled(tok[:, :3], par, x, u, t, 2)
+    with pytest.raises(ValueError):
+        api.accept_sampled(tok, par, x, u, t, 3)
+    with pytest.raises(ValueError):
+        api.accept_sampled(tok, par, x, u, t[:1], 2)
+    with pytest.raises(ValueError):
+        api.accept_sampled(tok, par, x[:, :, :7], u, t, 2)
+    with pytest.raises(ValueError):
+        api.accept_sampled(tok, par, x, u, t, 2, out=dict(accepted_len=z(2, dt=torch.int32), path=z(2, 4, dt=torch.int32),
+                                                          bonus=z(2, dt=torch.int32)))

@@ -1,4 +1,4 @@
-"""ctypes binding of libjf.so (include/jf.h).  Argument marshalling only: every step of the hot path
+"""ctypes binding of libjf.so (include/jf.h, include/jf_serving.h).  Argument marshalling only: every step of the hot path
 runs in the library's CUDA kernels.  There is no fallback: if the library is missing or cannot be
 loaded, :func:`lib` raises."""
 from __future__ import annotations
@@ -11,6 +11,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libjf.so")
 DEBUG_LIB_PATH = os.path.join(_PKG, "libjf_debug.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "jf.h")
+SERVING_HEADER = os.path.join(os.path.dirname(_PKG), "include", "jf_serving.h")
 DEBUG_HEADER = os.path.join(os.path.dirname(_PKG), "include", "jf_debug.h")
 
 JF_OK = 0
@@ -57,6 +58,7 @@ def _load(path: str) -> ctypes.CDLL:
         raise RuntimeError(f"{path} is missing: build it with `python -m tree_verify_attention_jf_b200.build`")
     L = ctypes.CDLL(path)
     vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    ll = ctypes.c_longlong
     L.jf_status_string.argtypes = [i]
     L.jf_status_string.restype = ctypes.c_char_p
     L.jf_version.argtypes = []
@@ -84,6 +86,10 @@ def _load(path: str) -> ctypes.CDLL:
     L.jf_commit_kv.restype = i
     L.jf_tree_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, vp, vp, i, i, i, i, i, i, i, f, vp, vp]
     L.jf_tree_kv_append.restype = i
+    L.jf_sample.argtypes = [vp, i, ll, i, i, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.jf_sample.restype = i
+    L.jf_accept_sampled.argtypes = [vp, vp, vp, i, vp, vp, vp, vp, vp, i, i, i, i, vp, vp, vp, vp, vp, vp]
+    L.jf_accept_sampled.restype = i
     return L
 
 

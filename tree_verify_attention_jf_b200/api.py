@@ -266,3 +266,100 @@ def tree_kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tens
                                         _ptr(depth), B, T, q.shape[1] if q is not None else 0, Hkv, D, page, num_pages,
                                         float(rope_theta), _ptr(dev_status), _stream(stream))
     _lib.check("jf_tree_kv_append", code)
+
+
+# ----------------------------------------------------------------------------------------------
+# Serving several sampled continuations of one prompt (include/jf_serving.h)
+# ----------------------------------------------------------------------------------------------
+_LOGITS_TYPE = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _call(fn: str, dev: torch.device, stream, *args) -> None:
+    """Calls a library function with ``dev`` current and, without a stream of the caller's, on that device's current
+    stream (the stream is the call's last argument)."""
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must live on a CUDA device, got {dev}")
+    s = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+    with torch.cuda.device(dev):
+        code = getattr(_lib.lib(), fn)(*args, s)
+    _lib.check(fn, code)
+
+
+def _sampling_params(n: int, dev: torch.device, temperature, top_k, top_p, min_p) -> list:
+    """Checks the per-row sampling parameters; top_k, top_p and min_p may be None (off)."""
+    for t, name, dtype in ((temperature, "temperature", torch.float32), (top_k, "top_k", torch.int32),
+                           (top_p, "top_p", torch.float32), (min_p, "min_p", torch.float32)):
+        if t is None and name != "temperature":
+            continue
+        _need(t, name, dtype, dev)
+        if t.shape != (n,):
+            raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
+    return [_ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p)]
+
+
+def _outputs(out: Optional[dict], dev: torch.device, **want) -> dict:
+    """``out`` after a check of the tensors it holds, or newly allocated ones; want: name=(shape, dtype).  The last
+    of the names, the log-probabilities, may be left out of ``out``."""
+    if out is None:
+        return {k: torch.empty(shape, dtype=dtype, device=dev) for k, (shape, dtype) in want.items()}
+    for k, (shape, dtype) in want.items():
+        if k == "logprob" and out.get(k) is None:
+            continue
+        _need(out[k], k, dtype, dev)
+        if tuple(out[k].shape) != shape:
+            raise ValueError(f"{k} must be {list(shape)}, got {list(out[k].shape)}")
+    return out
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor, top_k: Optional[torch.Tensor] = None,
+           top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+           dev_status: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """jf_sample: logits fp32 or bf16 [R, V] (rows may be strided, entries not), u and temperature fp32 [R] (u in
+    [0, 1); temperature 0 = greedy), top_k int32 [R] (0 = off), top_p fp32 [R] (1 = off), min_p fp32 [R] (0 = off), each
+    of the last three optional -> dict of token int32 [R] and logprob fp32 [R]."""
+    dev = logits.device
+    if logits.dtype not in _LOGITS_TYPE:
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    if logits.dim() != 2 or (logits.numel() and logits.stride(1) != 1):
+        raise ValueError("logits must be [R, V] with consecutive entries")
+    R, V = logits.shape
+    stride = logits.stride(0) if R > 1 else V
+    _need(u, "u", torch.float32, dev)
+    if u.shape != (R,):
+        raise ValueError(f"u must be [{R}], got {list(u.shape)}")
+    params = _sampling_params(R, dev, temperature, top_k, top_p, min_p)
+    out = _outputs(out, dev, token=((R,), torch.int32), logprob=((R,), torch.float32))
+    _call("jf_sample", dev, stream, _ptr(logits), _LOGITS_TYPE[logits.dtype], stride, R, V, _ptr(u), *params,
+          _ptr(out["token"]), _ptr(out.get("logprob")), _ptr(dev_status))
+    return out
+
+
+def accept_sampled(token: torch.Tensor, parent: torch.Tensor, target_logits: torch.Tensor, u: torch.Tensor,
+                   temperature: torch.Tensor, max_depth: int, top_k: Optional[torch.Tensor] = None,
+                   top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None,
+                   out: Optional[dict] = None, dev_status: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """jf_accept_sampled: :func:`accept` with a token sampled per step in place of the argmax.  token, parent int32
+    [B, N]; target_logits fp32 or bf16 [B, N, V]; u fp32 [B, max_depth + 1]; the parameters of :func:`sample` per
+    sequence, [B] -> dict of accepted_len int32 [B], path int32 [B, max_depth + 1], bonus int32 [B] and logprob fp32
+    [B, max_depth + 1] (of the token drawn at each step of the walk)."""
+    dev = target_logits.device
+    if target_logits.dtype not in _LOGITS_TYPE:
+        raise TypeError(f"target_logits must be float32 or bfloat16, got {target_logits.dtype}")
+    _need(target_logits, "target_logits", target_logits.dtype, dev)
+    if target_logits.dim() != 3:
+        raise ValueError("target_logits must be [B, N, V]")
+    B, N, V = target_logits.shape
+    for t, name in ((token, "token"), (parent, "parent")):
+        _need(t, name, torch.int32, dev)
+        if t.shape != (B, N):
+            raise ValueError(f"{name} must be [{B}, {N}], got {list(t.shape)}")
+    _need(u, "u", torch.float32, dev)
+    if max_depth < 0 or u.shape != (B, max_depth + 1):
+        raise ValueError(f"u must be [{B}, max_depth + 1] with max_depth >= 0, got {list(u.shape)}")
+    params = _sampling_params(B, dev, temperature, top_k, top_p, min_p)
+    out = _outputs(out, dev, accepted_len=((B,), torch.int32), path=((B, max_depth + 1), torch.int32),
+                   bonus=((B,), torch.int32), logprob=((B, max_depth + 1), torch.float32))
+    _call("jf_accept_sampled", dev, stream, _ptr(token), _ptr(parent), _ptr(target_logits),
+          _LOGITS_TYPE[target_logits.dtype], _ptr(u), *params, B, N, V, max_depth, _ptr(out["accepted_len"]),
+          _ptr(out["path"]), _ptr(out["bonus"]), _ptr(out.get("logprob")), _ptr(dev_status))
+    return out

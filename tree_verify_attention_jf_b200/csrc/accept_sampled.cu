@@ -1,0 +1,143 @@
+// accept_sampled.cu -- jf_accept_sampled: the acceptance walk over the verified draft tree with a sampled token in
+// place of the target's argmax (sm_100a, SIMT + clusters).
+//
+// Design: the walk is a chain of dependent draws, so latency matters.  One cluster per sequence; each step brings the
+// current node's row into the cluster's shared memory and draws from it (sampling.cuh); every CTA knows the token drawn
+// and finds the same child in its own copy of the tree.
+#include "sampling.cuh"
+
+namespace jf {
+namespace smp {
+
+struct Tree {
+  int tok[kMaxAcceptNodes], par[kMaxAcceptNodes];
+  int kid[2];  // the child found, by step parity
+};
+constexpr size_t kTreeOff = kSliceOff;
+constexpr size_t kWalkSliceOff = (kTreeOff + sizeof(Tree) + 127) & ~size_t(127);
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    accept_sampled_kernel(const int32_t* __restrict__ token, const int32_t* __restrict__ parent,
+                          const T* __restrict__ logits, const float* __restrict__ u, const SampleParams sp,
+                          int num_nodes, int vocab, int max_depth, int32_t* __restrict__ accepted_len,
+                          int32_t* __restrict__ path, int32_t* __restrict__ bonus, float* __restrict__ logprob,
+                          int32_t* status) {
+  extern __shared__ __align__(128) uint8_t raw[];
+  __shared__ int s_path[kMaxAcceptNodes + 1];
+  __shared__ float s_lp[kMaxAcceptNodes];
+  Smem& s = *reinterpret_cast<Smem*>(raw);
+  Tree& t = *reinterpret_cast<Tree*>(raw + kTreeOff);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const long long b = blockIdx.x / C;
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    mbar_init(&s.bar, 1);
+    fence_barrier_init();
+  }
+  if (tid < 128) s.tab[tid] = g_exp2_frac128[tid];
+  Row<T> row(s, raw + kWalkSliceOff, rank, C, vocab);
+  cluster.sync();  // every CTA of the cluster runs (remote shared memory may be written); the barrier is initialised
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before this one has completed
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const T* rows = logits + b * num_nodes * vocab;
+  const float* ub = u + b * (max_depth + 1);
+  bool bad = false;
+  for (int i = tid; i < num_nodes; i += kThreads) {
+    const int pi = __ldg(parent + b * num_nodes + i);
+    t.par[i] = pi;
+    t.tok[i] = __ldg(token + b * num_nodes + i);
+    bad = bad || pi < -1 || pi >= i;
+  }
+  RowParams rp;
+  bad = __syncthreads_or(bad) || !read_params(sp, b, rp);  // the same in every CTA of the cluster
+  if (bad) {
+    if (rank == 0 && tid == 0) report(status, JF_ERR_DEVICE_CHECK);
+    return;
+  }
+  int cur = 0, L = 0, drawn = -1;
+  for (int step = 0;; ++step) {
+    const float us = __ldg(ub + step);  // step == L <= max_depth
+    if (!good_u(us)) {
+      if (rank == 0 && tid == 0) report(status, JF_ERR_DEVICE_CHECK);
+      return;  // between two draws no CTA writes into another's shared memory
+    }
+    if (tid == 0) t.kid[step & 1] = INT_MAX;
+    fence_proxy_async_smem();
+    __syncthreads();  // the previous row's last reads are done before the copy of this one starts
+    row.start(rows + static_cast<long long>(cur) * vocab);
+    const Drawn d = row.draw(rp, us, step & 1);
+    if (!d.ok) {
+      volatile int never = 0;
+      mbar_wait(&s.bar, step & 1, &never);  // no copy of this CTA is left in flight
+      if (rank == 0 && tid == 0) report(status, JF_ERR_TIMEOUT);
+      return;
+    }
+    drawn = d.token;
+    if (tid == 0) {
+      s_path[L] = cur;
+      s_lp[L] = d.logprob;
+    }
+    if (L == max_depth || drawn < 0) break;
+    for (int c = tid; c < num_nodes; c += kThreads)
+      if (t.par[c] == cur && t.tok[c] == drawn) atomicMin(&t.kid[step & 1], c);
+    __syncthreads();
+    const int kid = t.kid[step & 1];
+    if (kid == INT_MAX) break;
+    cur = kid;
+    ++L;
+  }
+  if (rank != 0) return;
+  __syncthreads();
+  if (tid == 0) {
+    accepted_len[b] = L;
+    bonus[b] = drawn;
+  }
+  for (int i = tid; i <= max_depth; i += kThreads) {
+    path[b * (max_depth + 1) + i] = i <= L ? s_path[i] : -1;
+    if (logprob != nullptr) logprob[b * (max_depth + 1) + i] = i <= L ? s_lp[i] : 0.f;
+  }
+}
+
+template <typename T>
+cudaError_t launch_walk(const int32_t* token, const int32_t* parent, const T* logits, const float* u,
+                        const SampleParams& sp, int batch, int num_nodes, int vocab, int max_depth,
+                        int32_t* accepted_len, int32_t* path, int32_t* bonus, float* logprob, int32_t* status,
+                        cudaStream_t stream) {
+  static std::atomic<bool> attr_set[kMaxDevices];
+  const int dev = current_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    cudaError_t e = cudaFuncSetAttribute(accept_sampled_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(accept_sampled_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem);
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  // the widest cluster that leaves every CTA a slice worth its threads
+  int cluster = 1;
+  while (cluster < kMaxCluster && slice_len(vocab, cluster) > 2 * kThreads) cluster *= 2;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  return launch_pdl(accept_sampled_kernel<T>, dim3(static_cast<unsigned>(batch) * cluster), dim3(kThreads),
+                    kWalkSliceOff + slice_bytes(vocab, cluster, sizeof(T)), stream, &attr, token, parent, logits, u, sp,
+                    num_nodes, vocab, max_depth, accepted_len, path, bonus, logprob, status);
+}
+
+}  // namespace smp
+
+cudaError_t launch_accept_sampled(const int32_t* token, const int32_t* parent, const void* logits, bool bf16,
+                                  const float* u, const SampleParams& sp, int batch, int num_nodes, int vocab,
+                                  int max_depth, int32_t* accepted_len, int32_t* path, int32_t* bonus, float* logprob,
+                                  int32_t* status, cudaStream_t stream) {
+  return bf16 ? smp::launch_walk(token, parent, static_cast<const __nv_bfloat16*>(logits), u, sp, batch, num_nodes,
+                                 vocab, max_depth, accepted_len, path, bonus, logprob, status, stream)
+              : smp::launch_walk(token, parent, static_cast<const float*>(logits), u, sp, batch, num_nodes, vocab,
+                                 max_depth, accepted_len, path, bonus, logprob, status, stream);
+}
+
+}  // namespace jf
