@@ -17,6 +17,56 @@
 extern "C" {
 #endif
 
+/* ------------------------------------------------------------------------------------------
+ * jf_tree_attention_shared -- tree attention of a batch whose sequences share long prefixes.
+ *
+ * The attention of jf_tree_attention, for a batch that consists of groups of consecutive sequences
+ * (several continuations of one prompt): the sequences of group g hold the same first
+ * shared_lens[g] tokens, so their K/V up to there is the same, and with S = shared_lens[g] rounded
+ * down to whole pages the slots [0, S) of every sequence of the group are read through the block
+ * table row of the group's FIRST sequence, once for all nodes of the group.  Slots from S on are
+ * each sequence's own.  Block tables that agree on their first S / 16 entries, as prefix sharing
+ * gives them, therefore yield jf_tree_attention's result; the entries before S / 16 of the other
+ * rows are not read.  A group of one sequence, or one that shares nothing (shared_lens[g] = 0), is
+ * allowed; sequences without nodes are too.  For query rows the two parts' softmax states are joined
+ * in float32 before the one rounding to bf16.
+ *
+ * Layouts: as jf_tree_attention, and group_offsets int32 [num_groups+1], group_offsets[0] = 0,
+ *          non-decreasing, group_offsets[num_groups] = batch; shared_lens int32 [num_groups], >= 0.
+ * Limits: as jf_tree_attention, and batch + num_groups <= 1024, 1 <= num_groups <= batch.
+ * Device checks (JF_ERR_DEVICE_CHECK): those of jf_tree_attention; a sequence whose prefix is
+ *          shorter than its group's shared_lens is left unwritten; a page id out of range among the
+ *          shared ones, or more of them than the block table holds, leaves the whole group unwritten;
+ *          malformed group_offsets or a negative shared_lens leave the batch unwritten.
+ * workspace: jf_tree_attention_shared_workspace_size(total_nodes, num_q_heads) bytes, 256-byte
+ *          aligned, no initialisation; reusable by consecutive calls on one stream, also by calls of
+ *          fewer nodes and heads.
+ * ------------------------------------------------------------------------------------------ */
+JF_API size_t jf_tree_attention_shared_workspace_size(int total_nodes, int num_q_heads);
+
+JF_API jf_status jf_tree_attention_shared(const void* q, const void* k_cache, const void* v_cache,
+                                          const int32_t* block_table, int max_pages_per_seq,
+                                          const int32_t* prefix_lens, const int32_t* tree_offsets,
+                                          const int32_t* parent, const int32_t* group_offsets,
+                                          const int32_t* shared_lens, int num_groups, int batch, int total_nodes,
+                                          int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                                          int num_pages, float sm_scale, void* out, float* lse, void* workspace,
+                                          size_t workspace_bytes, int32_t* dev_status, jf_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * jf_tree_attention_shared_fp8 -- jf_tree_attention_shared over an 8-bit (E4M3) cache, as
+ * jf_tree_attention_fp8 stands to jf_tree_attention: uint8 caches, one scale > 0 for each.
+ * ------------------------------------------------------------------------------------------ */
+JF_API jf_status jf_tree_attention_shared_fp8(const void* q, const void* k_cache, const void* v_cache, float k_scale,
+                                              float v_scale, const int32_t* block_table, int max_pages_per_seq,
+                                              const int32_t* prefix_lens, const int32_t* tree_offsets,
+                                              const int32_t* parent, const int32_t* group_offsets,
+                                              const int32_t* shared_lens, int num_groups, int batch,
+                                              int total_nodes, int num_q_heads, int num_kv_heads, int head_dim,
+                                              int page_size, int num_pages, float sm_scale, void* out, float* lse,
+                                              void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                              jf_stream_t stream);
+
 typedef enum {
   JF_LOGITS_F32 = 0,
   JF_LOGITS_BF16 = 1

@@ -15,7 +15,8 @@ def L():
 
 def test_both_builds_export_every_declared_symbol(L):
     names = _lib.declared_functions(_lib.SERVING_HEADER)
-    assert {"jf_sample", "jf_accept_sampled"} <= set(names)
+    assert set(names) == {"jf_sample", "jf_accept_sampled", "jf_tree_attention_shared_workspace_size",
+                          "jf_tree_attention_shared", "jf_tree_attention_shared_fp8"}
     for n in names:
         assert hasattr(L, n) and hasattr(_lib.debug_lib(), n), n
 
@@ -53,6 +54,33 @@ def test_accept_sampled_host_validation(L):
         assert call(**bad) == BAD, bad
     for big in (dict(N=1025), dict(D=1024), dict(V=524289), dict(B=(1 << 24) + 1)):
         assert call(**big) == UNSUP, big
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_attention_shared_host_validation(L, fp8):
+    # the valid call has no nodes, so nothing is ever launched; with nodes, a null or short argument stops the call
+    def call(**o):
+        a = dict(q=16, k=32, v=48, ks=0.1, vs=0.1, bt=64, maxp=4, pl=64, to=64, par=64, go=64, sl=64, G=2, B=3, T=0, hq=4,
+                 hkv=1, d=128, page=16, pages=8, scale=0.1, out=64, ws=256,
+                 wsb=L.jf_tree_attention_shared_workspace_size(10, 4))
+        a.update(o)
+        fn = L.jf_tree_attention_shared_fp8 if fp8 else L.jf_tree_attention_shared
+        return fn(a["q"], a["k"], a["v"], *((a["ks"], a["vs"]) if fp8 else ()), a["bt"], a["maxp"], a["pl"], a["to"],
+                  a["par"], a["go"], a["sl"], a["G"], a["B"], a["T"], a["hq"], a["hkv"], a["d"], a["page"], a["pages"],
+                  a["scale"], a["out"], None, a["ws"], a["wsb"], None, None)
+    assert call() == OK
+    assert call(B=0, G=0, T=5) == OK
+    for null in ("q", "k", "v", "bt", "pl", "to", "par", "go", "sl", "out", "ws"):
+        assert call(T=10, **{null: None}) == BAD, null
+    for bad in (dict(G=-1), dict(G=4), dict(G=0, T=10), dict(scale=0.0), dict(hkv=0), dict(T=10, q=24),
+                dict(T=10, ws=257), dict(T=10, wsb=100), dict(T=11)):
+        assert call(**bad) == BAD, bad
+    for bad in (dict(d=64), dict(page=32), dict(hq=6, hkv=4), dict(B=1000, G=25), dict(pages=1 << 27)):
+        assert call(**bad) == UNSUP, bad
+    if fp8:
+        assert call(ks=0.0) == BAD and call(vs=float("nan")) == BAD
+    size = L.jf_tree_attention_shared_workspace_size
+    assert size(10, 4) < size(11, 4) < size(11, 32) and size(10, 4) % 256 == 0
 
 
 def test_python_calls_refuse_cpu_tensors():

@@ -86,6 +86,14 @@ def _load(path: str) -> ctypes.CDLL:
     L.jf_commit_kv.restype = i
     L.jf_tree_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, vp, vp, i, i, i, i, i, i, i, f, vp, vp]
     L.jf_tree_kv_append.restype = i
+    L.jf_tree_attention_shared_workspace_size.argtypes = [i, i]
+    L.jf_tree_attention_shared_workspace_size.restype = sz
+    L.jf_tree_attention_shared.argtypes = [vp, vp, vp, vp, i, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp, vp, vp,
+                                           sz, vp, vp]
+    L.jf_tree_attention_shared.restype = i
+    L.jf_tree_attention_shared_fp8.argtypes = [vp, vp, vp, f, f, vp, i, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp,
+                                               vp, vp, sz, vp, vp]
+    L.jf_tree_attention_shared_fp8.restype = i
     L.jf_sample.argtypes = [vp, i, ll, i, i, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.jf_sample.restype = i
     L.jf_accept_sampled.argtypes = [vp, vp, vp, i, vp, vp, vp, vp, vp, i, i, i, i, vp, vp, vp, vp, vp, vp]

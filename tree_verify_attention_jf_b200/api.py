@@ -363,3 +363,85 @@ def accept_sampled(token: torch.Tensor, parent: torch.Tensor, target_logits: tor
           _LOGITS_TYPE[target_logits.dtype], _ptr(u), *params, B, N, V, max_depth, _ptr(out["accepted_len"]),
           _ptr(out["path"]), _ptr(out["bonus"]), _ptr(out.get("logprob")), _ptr(dev_status))
     return out
+
+
+class SharedAttentionWorkspace:
+    """Scratch for :func:`tree_attention_shared` calls of up to ``total_nodes`` tree nodes with ``num_q_heads`` heads.
+    One per stream; needs no initialisation and is reusable across calls."""
+
+    def __init__(self, total_nodes: int, num_q_heads: int, device):
+        n = _lib.lib().jf_tree_attention_shared_workspace_size(total_nodes, num_q_heads)
+        self.buf = torch.empty(n, dtype=torch.uint8, device=device)
+
+    @property
+    def nbytes(self) -> int:
+        return self.buf.numel()
+
+
+def _attention_shared(fn, cache_dtype, scales, q, k_cache, v_cache, block_table, prefix_lens, tree_offsets, parent,
+                      group_offsets, shared_lens, sm_scale, out, lse, workspace, dev_status, stream):
+    dev = q.device
+    _need(q, "q", torch.bfloat16, dev)
+    _need(k_cache, "k_cache", cache_dtype, dev)
+    _need(v_cache, "v_cache", cache_dtype, dev)
+    for name, t in (("block_table", block_table), ("prefix_lens", prefix_lens), ("tree_offsets", tree_offsets),
+                    ("parent", parent), ("group_offsets", group_offsets), ("shared_lens", shared_lens)):
+        _need(t, name, torch.int32, dev)
+    if q.dim() != 3 or k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("q must be [T, Hq, 128], k_cache and v_cache both [pages, 16, Hkv, 128]")
+    T, Hq, D = q.shape
+    num_pages, page, Hkv, cache_dim = k_cache.shape
+    B, G = prefix_lens.numel(), shared_lens.numel()
+    if cache_dim != D:
+        raise ValueError("q and the caches have different head dimensions")
+    if block_table.dim() != 2 or block_table.shape[0] != B or tree_offsets.numel() != B + 1:
+        raise ValueError("block_table must be [B, max_pages] and tree_offsets [B + 1]")
+    if group_offsets.numel() != G + 1 or parent.numel() != T:
+        raise ValueError("group_offsets must be [G + 1] for G shared_lens, parent [T]")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", torch.bfloat16, dev)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, dev)
+        if lse.shape != (T, Hq):
+            raise ValueError("lse must be [T, Hq]")
+    if workspace is None:
+        workspace = SharedAttentionWorkspace(T, Hq, dev)
+        if stream is not None:  # the call runs on another stream than the one the scratch was allocated on
+            workspace.buf.record_stream(torch.cuda.ExternalStream(_stream(stream), device=dev))
+    _call(fn, dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), *scales, _ptr(block_table), block_table.shape[1],
+          _ptr(prefix_lens), _ptr(tree_offsets), _ptr(parent), _ptr(group_offsets), _ptr(shared_lens), G, B, T, Hq, Hkv,
+          D, page, num_pages, float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace.buf), workspace.nbytes,
+          _ptr(dev_status))
+    return out
+
+
+def tree_attention_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                          prefix_lens: torch.Tensor, tree_offsets: torch.Tensor, parent: torch.Tensor,
+                          group_offsets: torch.Tensor, shared_lens: torch.Tensor, sm_scale: float,
+                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                          workspace: Optional[SharedAttentionWorkspace] = None,
+                          dev_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """jf_tree_attention_shared: :func:`tree_attention` of a batch made of groups of consecutive sequences, group g =
+    sequences [group_offsets[g], group_offsets[g + 1]) (int32 [G + 1]) with the first shared_lens[g] tokens (int32 [G])
+    in common; the whole pages of that prefix are read through the group's first block-table row, once for all its
+    nodes.  Returns out."""
+    return _attention_shared("jf_tree_attention_shared", torch.bfloat16, (), q, k_cache, v_cache, block_table,
+                             prefix_lens, tree_offsets, parent, group_offsets, shared_lens, sm_scale, out, lse, workspace,
+                             dev_status, stream)
+
+
+def tree_attention_shared_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float,
+                              v_scale: float, block_table: torch.Tensor, prefix_lens: torch.Tensor,
+                              tree_offsets: torch.Tensor, parent: torch.Tensor, group_offsets: torch.Tensor,
+                              shared_lens: torch.Tensor, sm_scale: float, out: Optional[torch.Tensor] = None,
+                              lse: Optional[torch.Tensor] = None,
+                              workspace: Optional[SharedAttentionWorkspace] = None,
+                              dev_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """jf_tree_attention_shared_fp8: as :func:`tree_attention_shared`, with k/v_cache uint8 E4M3 codes [pages, 16, Hkv,
+    128] standing for decode(code) * k_scale / v_scale.  Returns out (bf16)."""
+    return _attention_shared("jf_tree_attention_shared_fp8", torch.uint8, (float(k_scale), float(v_scale)), q, k_cache,
+                             v_cache, block_table, prefix_lens, tree_offsets, parent, group_offsets, shared_lens,
+                             sm_scale, out, lse, workspace, dev_status, stream)

@@ -6,7 +6,7 @@
 #include <mutex>
 
 #include "../../include/jf.h"
-#include "jf_internal.h"
+#include "serving_internal.h"
 
 namespace {
 
@@ -57,14 +57,16 @@ bool encode_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uin
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// jf_tree_attention and jf_tree_attention_fp8: validation, tensor maps, workspace carving, launch.
-jf_status tree_attention_call(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
-                              int max_pages_per_seq, const int32_t* prefix_lens, const int32_t* tree_offsets,
-                              const int32_t* parent, int batch, int total_nodes, int num_q_heads, int num_kv_heads,
-                              int head_dim, int page_size, int num_pages, float sm_scale, bool fp8, float k_scale,
-                              float v_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
-                              int32_t* dev_status, jf_stream_t stream) {
-  using namespace jf;
+}  // namespace
+
+namespace jf {
+
+jf_status attention_call(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                         int max_pages_per_seq, const int32_t* prefix_lens, const int32_t* tree_offsets,
+                         const int32_t* parent, const SharedArgs* shared, int batch, int total_nodes, int num_q_heads,
+                         int num_kv_heads, int head_dim, int page_size, int num_pages, float sm_scale, bool fp8,
+                         float k_scale, float v_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                         int32_t* dev_status, jf_stream_t stream) {
   if (batch < 0 || total_nodes < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_pages_per_seq <= 0 ||
       num_pages <= 0)
     return JF_ERR_INVALID_ARG;
@@ -76,15 +78,19 @@ jf_status tree_attention_call(const void* q, const void* k_cache, const void* v_
   if (num_q_heads % num_kv_heads != 0) return JF_ERR_UNSUPPORTED;
   const int group = num_q_heads / num_kv_heads;
   if (group != 1 && group != 2 && group != 4 && group != 8 && group != 16) return JF_ERR_UNSUPPORTED;
-  if (batch > kMaxAttnBatch) return JF_ERR_UNSUPPORTED;
+  if (shared != nullptr && (shared->num_groups < 0 || shared->num_groups > batch)) return JF_ERR_INVALID_ARG;
+  if (batch + (shared != nullptr ? shared->num_groups : 0) > kMaxAttnBatch) return JF_ERR_UNSUPPORTED;
   if (static_cast<long long>(num_pages) * kPageSize >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
   if (batch == 0 || total_nodes == 0) return JF_OK;
   if (!q || !k_cache || !v_cache || !block_table || !prefix_lens || !tree_offsets || !parent || !out || !workspace)
     return JF_ERR_INVALID_ARG;
+  if (shared != nullptr && (shared->num_groups == 0 || !shared->group_offsets || !shared->shared_lens))
+    return JF_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
       !aligned(workspace, 256))
     return JF_ERR_INVALID_ARG;
-  if (workspace_bytes < AttnWorkspace::total) return JF_ERR_INVALID_ARG;
+  const SharedAttnWorkspace sw(total_nodes, num_q_heads);
+  if (workspace_bytes < (shared != nullptr ? sw.total : AttnWorkspace::total)) return JF_ERR_INVALID_ARG;
 
   const int sms = sm_count();
   if (sms <= 0) return JF_ERR_CUDA;
@@ -111,7 +117,7 @@ jf_status tree_attention_call(const void* q, const void* k_cache, const void* v_
   }
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  AttnParams p;
+  SharedAttnParams p{};
   p.block_table = block_table;
   p.prefix_lens = prefix_lens;
   p.tree_offsets = tree_offsets;
@@ -132,12 +138,20 @@ jf_status tree_attention_call(const void* q, const void* k_cache, const void* v_
   p.num_pages = num_pages;
   p.scale_log2 = sm_scale * k_scale * 1.4426950408889634f;
   p.v_scale = v_scale;
-  if (launch_tree_attention(tm_q, tm_k, tm_v, p, grid, fp8, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return JF_ERR_CUDA;
-  return JF_OK;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (shared == nullptr)
+    return launch_tree_attention(tm_q, tm_k, tm_v, p, grid, fp8, st) == cudaSuccess ? JF_OK : JF_ERR_CUDA;
+  p.group_offsets = shared->group_offsets;
+  p.shared_lens = shared->shared_lens;
+  p.num_groups = shared->num_groups;
+  p.cta_ok = reinterpret_cast<int32_t*>(ws + sw.ok_off);
+  p.rows_o = reinterpret_cast<float4*>(ws + sw.o_off);
+  p.rows_ml = reinterpret_cast<float2*>(ws + sw.ml_off);
+  p.rows_at = reinterpret_cast<int4*>(ws + sw.at_off);
+  return launch_tree_attention_shared(tm_q, tm_k, tm_v, p, grid, fp8, st) == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 
-}  // namespace
+}  // namespace jf
 
 extern "C" {
 
@@ -168,9 +182,9 @@ jf_status jf_tree_attention(const void* q, const void* k_cache, const void* v_ca
                             const int32_t* parent, int batch, int total_nodes, int num_q_heads, int num_kv_heads,
                             int head_dim, int page_size, int num_pages, float sm_scale, void* out, float* lse,
                             void* workspace, size_t workspace_bytes, int32_t* dev_status, jf_stream_t stream) {
-  return tree_attention_call(q, k_cache, v_cache, block_table, max_pages_per_seq, prefix_lens, tree_offsets, parent,
-                             batch, total_nodes, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, sm_scale,
-                             false, 1.f, 1.f, out, lse, workspace, workspace_bytes, dev_status, stream);
+  return jf::attention_call(q, k_cache, v_cache, block_table, max_pages_per_seq, prefix_lens, tree_offsets, parent,
+                            nullptr, batch, total_nodes, num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
+                            sm_scale, false, 1.f, 1.f, out, lse, workspace, workspace_bytes, dev_status, stream);
 }
 
 jf_status jf_tree_attention_fp8(const void* q, const void* k_cache, const void* v_cache, float k_scale,
@@ -179,9 +193,9 @@ jf_status jf_tree_attention_fp8(const void* q, const void* k_cache, const void* 
                                 int batch, int total_nodes, int num_q_heads, int num_kv_heads, int head_dim,
                                 int page_size, int num_pages, float sm_scale, void* out, float* lse, void* workspace,
                                 size_t workspace_bytes, int32_t* dev_status, jf_stream_t stream) {
-  return tree_attention_call(q, k_cache, v_cache, block_table, max_pages_per_seq, prefix_lens, tree_offsets, parent,
-                             batch, total_nodes, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, sm_scale,
-                             true, k_scale, v_scale, out, lse, workspace, workspace_bytes, dev_status, stream);
+  return jf::attention_call(q, k_cache, v_cache, block_table, max_pages_per_seq, prefix_lens, tree_offsets, parent,
+                            nullptr, batch, total_nodes, num_q_heads, num_kv_heads, head_dim, page_size, num_pages,
+                            sm_scale, true, k_scale, v_scale, out, lse, workspace, workspace_bytes, dev_status, stream);
 }
 
 size_t jf_build_tree_workspace_size(int batch, int depths, int vocab, int topk) {

@@ -10,6 +10,36 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 extern "C" {
 
+size_t jf_tree_attention_shared_workspace_size(int total_nodes, int num_q_heads) {
+  return jf::SharedAttnWorkspace(total_nodes > 0 ? total_nodes : 0, num_q_heads > 0 ? num_q_heads : 0).total;
+}
+
+jf_status jf_tree_attention_shared(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                                   int max_pages_per_seq, const int32_t* prefix_lens, const int32_t* tree_offsets,
+                                   const int32_t* parent, const int32_t* group_offsets, const int32_t* shared_lens,
+                                   int num_groups, int batch, int total_nodes, int num_q_heads, int num_kv_heads,
+                                   int head_dim, int page_size, int num_pages, float sm_scale, void* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, int32_t* dev_status, jf_stream_t stream) {
+  const jf::SharedArgs sh{group_offsets, shared_lens, num_groups};
+  return jf::attention_call(q, k_cache, v_cache, block_table, max_pages_per_seq, prefix_lens, tree_offsets, parent, &sh,
+                            batch, total_nodes, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, sm_scale,
+                            false, 1.f, 1.f, out, lse, workspace, workspace_bytes, dev_status, stream);
+}
+
+jf_status jf_tree_attention_shared_fp8(const void* q, const void* k_cache, const void* v_cache, float k_scale,
+                                       float v_scale, const int32_t* block_table, int max_pages_per_seq,
+                                       const int32_t* prefix_lens, const int32_t* tree_offsets, const int32_t* parent,
+                                       const int32_t* group_offsets, const int32_t* shared_lens, int num_groups,
+                                       int batch, int total_nodes, int num_q_heads, int num_kv_heads, int head_dim,
+                                       int page_size, int num_pages, float sm_scale, void* out, float* lse,
+                                       void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                       jf_stream_t stream) {
+  const jf::SharedArgs sh{group_offsets, shared_lens, num_groups};
+  return jf::attention_call(q, k_cache, v_cache, block_table, max_pages_per_seq, prefix_lens, tree_offsets, parent, &sh,
+                            batch, total_nodes, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, sm_scale,
+                            true, k_scale, v_scale, out, lse, workspace, workspace_bytes, dev_status, stream);
+}
+
 jf_status jf_sample(const void* logits, int logits_type, long long row_stride, int rows, int vocab, const float* u,
                     const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                     int32_t* token, float* logprob, int32_t* dev_status, jf_stream_t stream) {

@@ -27,11 +27,17 @@
 //     in a descriptor slot; combine_kernel, launched right behind on the
 //     same stream with a programmatic dependency, merges each recorded unit's partials and stores the
 //     bf16 output.  Nothing spins on another CTA.
+//   * Shared prefix (jf_tree_attention_shared): the same kernel over two kinds of items.  A group item has the rows of
+//     all of a group's sequences and the keys of the prefix they share, so that a K/V tile is read once for all of them
+//     and its M tiles are full even when every sequence has one node; a sequence item has one sequence's rows and
+//     the rest of its keys.  Every row then has two softmax states, which shared_combine_kernel joins.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "jf_device.cuh"
-#include "jf_internal.h"
+#include "serving_internal.h"
 
 namespace jf {
 #ifdef JF_DEBUG
@@ -56,6 +62,14 @@ constexpr uint32_t kTmO = 256;  // O_i at column 256 + 128 * i
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P may grow up to 2^8 before O is rescaled
 constexpr int kSegCost = 3;  // kv tiles' worth of time that starting a segment in mid-kernel costs
 
+// What a kernel instantiation computes: the cache's type, and one item per sequence or, with a shared prefix, items of
+// groups [0, num_groups) followed by items of sequences.
+template <bool Fp8, bool Shared>
+struct Mode {
+  static constexpr bool kFp8 = Fp8, kShared = Shared;
+  using Params = std::conditional_t<Shared, SharedAttnParams, AttnParams>;
+};
+
 struct __align__(1024) Smem {
   uint8_t q[kAttnQTiles][kTileBytes];
   uint8_t k[kStages][kTileBytes];
@@ -65,6 +79,10 @@ struct __align__(1024) Smem {
   long long cum_work[kMaxAttnBatch + 1];
   int seq_p[kMaxAttnBatch];       // prefix length of every sequence (copied once by the plan)
   int seq_off[kMaxAttnBatch + 1]; // tree_offsets
+  // shared prefix, where item i takes the place of sequence i and seq_p, seq_off are its keys before the tree and its
+  // first node: nodes, and a group's first sequence or the whole pages that a sequence item leaves out (-1: lengths
+  // that contradict each other or the block table)
+  int item_n[kMaxAttnBatch], item_x[kMaxAttnBatch];
   long long scan_warp[kThreads / 32];
   uint64_t bar_qfull, bar_qempty;
   uint64_t bar_kfull[kStages], bar_kempty[kStages], bar_vfull[kStages], bar_vempty[kStages];
@@ -84,6 +102,8 @@ struct __align__(1024) Smem {
 struct Seg {
   int b, kvh, mp, kb, ke;  // positions [kb, ke) of unit (b, kvh, M-tile pair mp)
   int P, N, off, kt;       // prefix length, nodes, first global node, kv tiles of the sequence
+  int rows;                // nodes that have rows: N, or those of a whole group, whose item has no tree keys (N = 0)
+  int row, page0, pages;   // row of the block table, first page of the item in it, pages from there on
   int c0, c1, slot;        // CTAs sharing the unit; this CTA's partial slot (times kAttnQTiles)
   int rot;                 // the unit's rotation: position t reads kv tile (t - rot) mod kt
   __device__ __forceinline__ int tile(int t) const {
@@ -112,19 +132,34 @@ __device__ __forceinline__ int pairs_of(int N, int group) {
 // rate, so at local time x a CTA reads tile x or tile x + (kt - W / G) of its unit: the M-tile pairs of one
 // (sequence, kv head), which read the same K and V, do so at two offsets instead of one offset each, and the
 // later readers find most of the tiles in L2.  Any rotation keeps the pieces of a unit disjoint.
+template <class M>
 struct SegIter {
   long long x, xend, W;
   int G, b;
-  __device__ bool next(const Smem& s, const AttnParams& p, Seg& g) {
+  __device__ bool next(const Smem& s, const typename M::Params& p, Seg& g) {
     while (x < xend) {
       while (s.cum_work[b + 1] <= x) ++b;
       g.b = b;
       g.P = s.seq_p[b];
       g.off = s.seq_off[b];
-      g.N = s.seq_off[b + 1] - g.off;
+      if constexpr (M::kShared) {
+        const int ix = s.item_x[b];
+        const bool grp = b < p.num_groups;
+        g.rows = s.item_n[b];
+        g.N = grp ? 0 : g.rows;
+        g.row = grp ? (ix < 0 ? 0 : ix) : b - p.num_groups;
+        g.page0 = grp || ix < 0 ? 0 : ix;
+        g.pages = p.max_pages - g.page0;
+      } else {
+        g.N = s.seq_off[b + 1] - g.off;
+        g.rows = g.N;
+        g.row = b;
+        g.page0 = 0;
+        g.pages = p.max_pages;
+      }
       g.kt = (g.P + g.N + kBN - 1) / kBN;
       const long long span = g.kt + kSegCost;
-      const int mpn = pairs_of(g.N, p.group);
+      const int mpn = pairs_of(g.rows, p.group);
       const long long unit = (x - s.cum_work[b]) / span;
       const long long u0 = s.cum_work[b] + unit * span, u1 = u0 + span;
       const long long e = xend < u1 ? xend : u1;
@@ -153,8 +188,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ void set_abort(Smem& s, const AttnParams& p) {
+template <class M>
+__device__ __forceinline__ void set_abort(Smem& s, const typename M::Params& p) {
   *reinterpret_cast<volatile int*>(&s.abort_flag) = 1;
+  if constexpr (M::kShared) __stcg(&p.cta_ok[blockIdx.x], 0);
   report(p.status, JF_ERR_TIMEOUT);
 }
 
@@ -219,6 +256,81 @@ __device__ void build_plan(Smem& s, const AttnParams& p) {
   __syncthreads();
 }
 
+// The plan with a shared prefix: the same over the items (num_groups + batch <= kMaxAttnBatch).  Whole pages only
+// are shared, so that a sequence item starts on a page: the last, partial page is read by every sequence itself.
+__device__ void build_shared_plan(Smem& s, const SharedAttnParams& p) {
+  const int tid = threadIdx.x;
+  const int B = p.batch, G = p.num_groups, I = G + B;
+  if (tid == 0) s.bad_meta = 0;
+  __syncthreads();
+  int bad = 0;
+  if (tid == 0 && (p.tree_offsets[0] != 0 || p.tree_offsets[B] != p.total_nodes || p.group_offsets[0] != 0 ||
+                   p.group_offsets[G] != B))
+    bad = 1;
+  for (int g = tid; g < G; g += kThreads) {
+    const int b0 = p.group_offsets[g], b1 = p.group_offsets[g + 1], len = p.shared_lens[g];
+    s.item_x[g] = s.item_n[g] = s.seq_p[g] = s.seq_off[g] = 0;
+    if (b0 < 0 || b1 < b0 || b1 > B || len < 0) {
+      bad = 1;
+      continue;
+    }
+    if (b0 == b1) continue;  // no sequences: no rows
+    const int o0 = p.tree_offsets[b0], n = p.tree_offsets[b1] - o0, shared = len / kPage;
+    const bool fits = shared <= p.max_pages;
+    s.item_x[g] = fits ? b0 : -1;
+    s.item_n[g] = shared > 0 && n > 0 ? n : 0;
+    s.seq_p[g] = fits ? shared * kPage : kPage;
+    s.seq_off[g] = o0;
+  }
+  if (bad) atomicOr(&s.bad_meta, 1);
+  __syncthreads();
+  if (s.bad_meta) return;
+  for (int b = tid; b < B; b += kThreads) {
+    int lo = 0, hi = G - 1;  // the last group that starts at or before b
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.group_offsets[mid] <= b) lo = mid; else hi = mid - 1;
+    }
+    const int P = p.prefix_lens[b], off = p.tree_offsets[b], N = p.tree_offsets[b + 1] - off;
+    const int shared = p.shared_lens[lo] / kPage;
+    if (P < 0 || N < 0 || N > kMaxTreeNodes || p.group_offsets[lo] > b || p.group_offsets[lo + 1] <= b) bad = 1;
+    // what is shared is part of the sequence's prefix, and its table has room for the slots; the item of one that
+    // says otherwise is walked over its first pages and not stored
+    const bool fits = P >= p.shared_lens[lo] && static_cast<long long>(P) + N <= static_cast<long long>(p.max_pages) * kPage;
+    s.item_x[G + b] = fits ? shared : -1;
+    s.seq_p[G + b] = fits ? P - shared * kPage : 0;
+    s.seq_off[G + b] = off;
+    s.item_n[G + b] = N;
+  }
+  if (bad) atomicOr(&s.bad_meta, 1);
+  __syncthreads();
+  if (s.bad_meta) return;
+  const int per = (I + kThreads - 1) / kThreads;
+  const int i0 = tid * per;
+  auto cost = [&](int i) {
+    if (s.item_n[i] == 0) return 0ll;
+    const long long kt = (static_cast<long long>(s.seq_p[i]) + (i < G ? 0 : s.item_n[i]) + kBN - 1) / kBN;
+    return static_cast<long long>(p.hkv) * pairs_of(s.item_n[i], p.group) * (kt + kSegCost);
+  };
+  long long local = 0;
+  for (int i = i0; i < i0 + per && i < I; ++i) local += cost(i);
+  long long incl = local;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if ((tid & 31) >= o) incl += v;
+  }
+  if ((tid & 31) == 31) s.scan_warp[tid >> 5] = incl;
+  __syncthreads();
+  long long run = incl - local;
+  for (int w = 0; w < (tid >> 5); ++w) run += s.scan_warp[w];
+  for (int i = i0; i < i0 + per && i < I; ++i) {
+    s.cum_work[i] = run;
+    run += cost(i);
+  }
+  if (tid == kThreads - 1) s.cum_work[I] = run;
+  __syncthreads();
+}
+
 // ------------------------------------------------------------------------------------------------
 // 8-bit (E4M3) cache: conversion to f16 in shared memory.  Every E4M3 value is exactly an f16, so the MMAs
 // run on f16 operands (Q converted from bf16, which it also represents exactly in the range of attention
@@ -280,9 +392,10 @@ __device__ __forceinline__ void convert_q_bf16_f16(uint8_t* q, int bytes, int la
 // at a time, and arrives on the full barrier the MMA warp waits on once a tile is done (the Q tiles are
 // converted right after the segment's first K tile is issued).
 // ------------------------------------------------------------------------------------------------
-template <bool kFp8>
-__device__ void kv_producer(Smem& s, const AttnParams& p, SegIter iter, bool is_v, const CUtensorMap* tm_q,
+template <class M>
+__device__ void kv_producer(Smem& s, const typename M::Params& p, SegIter<M> iter, bool is_v, const CUtensorMap* tm_q,
                             const CUtensorMap* tm_kv) {
+  constexpr bool kFp8 = M::kFp8;
   const int lane = threadIdx.x & 31;
   volatile int* abort = &s.abort_flag;
   uint64_t* full = is_v ? s.bar_vfull : s.bar_kfull;
@@ -298,7 +411,7 @@ __device__ void kv_producer(Smem& s, const AttnParams& p, SegIter iter, bool is_
   // the Q landing barrier: on an abort the warp waits for them, i.e. for every copy it issued
   uint32_t armed = 0, armed_par = 0, q_armed = 0, q_par = 0;
   auto unwind = [&]() {
-    set_abort(s, p);
+    set_abort<M>(s, p);
     for (int st = 0; st < kStages; ++st)
       if (armed & (1u << st)) drain_wait(&land[st], (armed_par >> st) & 1u);
     if (q_armed) drain_wait(qland, q_par);
@@ -334,7 +447,7 @@ __device__ void kv_producer(Smem& s, const AttnParams& p, SegIter iter, bool is_
   const int nodes_per_tile = kBM / p.group;
   while (iter.next(s, p, g)) {
     const int npg = (g.P + g.N + kPage - 1) / kPage;
-    const int32_t* bt = p.block_table + static_cast<long long>(g.b) * p.max_pages;
+    const int32_t* bt = p.block_table + static_cast<long long>(g.row) * p.max_pages + g.page0;
     // Page ids are fetched four positions at a time (lane l: logical page 8 * tile(t0 + l / 8) + l % 8, -1 = not
     // loaded) and one batch ahead, so the block-table latency stays off the issue path.
     auto batch_ids = [&](int t0) {
@@ -342,7 +455,7 @@ __device__ void kv_producer(Smem& s, const AttnParams& p, SegIter iter, bool is_
       const int t = t0 + (lane >> 3);
       if (t < g.ke) {
         const int pg = g.tile(t) * kPagesPerTile + (lane & 7);
-        if (pg < npg && pg < p.max_pages) {
+        if (pg < npg && pg < g.pages) {
           const int v = __ldg(bt + pg);
           if (v >= 0 && v < p.num_pages) pid = v;
         }
@@ -474,15 +587,16 @@ __device__ __forceinline__ void issue_pv(const Smem& s, uint32_t tmem, int qt, i
   }
 }
 
-template <bool kFp8>
-__device__ void mma_issuer(Smem& s, const AttnParams& p, SegIter iter, uint32_t tmem) {
+template <class M>
+__device__ void mma_issuer(Smem& s, const typename M::Params& p, SegIter<M> iter, uint32_t tmem) {
+  constexpr bool kFp8 = M::kFp8;
   const int lane = threadIdx.x & 31;
   volatile int* abort = &s.abort_flag;
   Seg g;
   uint32_t it = 0, sidx = 0;
   bool issued = false;
   auto unwind = [&]() {  // the last MMA issued completes before the CTA releases its tensor memory
-    set_abort(s, p);
+    set_abort<M>(s, p);
     if (issued) {
       if (lane == 0) mma_commit(&s.bar_drain);
       __syncwarp();
@@ -555,7 +669,8 @@ __device__ void mma_issuer(Smem& s, const AttnParams& p, SegIter iter, uint32_t 
 // ------------------------------------------------------------------------------------------------
 // Warp 3: per-segment validation
 // ------------------------------------------------------------------------------------------------
-__device__ void metadata(Smem& s, const AttnParams& p, SegIter iter) {
+template <class M>
+__device__ void metadata(Smem& s, const typename M::Params& p, SegIter<M> iter) {
   const int lane = threadIdx.x & 31;
   volatile int* abort = &s.abort_flag;
   Seg g;
@@ -565,7 +680,7 @@ __device__ void metadata(Smem& s, const AttnParams& p, SegIter iter) {
     if (lane == 0) {
       const bool ok = mbar_wait(&s.bar_metaempty[buf], ((sidx >> 1) & 1) ^ 1, abort);
       s.meta_ctl = ok ? 1 : 0;
-      if (!ok) set_abort(s, p);
+      if (!ok) set_abort<M>(s, p);
     }
     __syncwarp();
     if (s.meta_ctl == 0) return;
@@ -573,14 +688,15 @@ __device__ void metadata(Smem& s, const AttnParams& p, SegIter iter) {
     // the segment is issued before any is used, so the whole check costs one memory round trip.
     const int npg = (g.P + g.N + kPage - 1) / kPage;
     const int32_t* par = p.parent + g.off;
-    const int32_t* bt = p.block_table + static_cast<long long>(g.b) * p.max_pages;
+    const int32_t* bt = p.block_table + static_cast<long long>(g.row) * p.max_pages + g.page0;
     int pr[kMaxTreeNodes / 32];
 #pragma unroll
     for (int k = 0; k < kMaxTreeNodes / 32; ++k) {
       const int i = lane + 32 * k;
       pr[k] = i < g.N ? __ldg(par + i) : -1;
     }
-    int bad = (static_cast<long long>(g.P) + g.N > static_cast<long long>(p.max_pages) * kPage) ? 1 : 0;
+    int bad = (static_cast<long long>(g.P) + g.N > static_cast<long long>(g.pages) * kPage) ? 1 : 0;
+    if constexpr (M::kShared) bad |= s.item_x[g.b] < 0 ? 1 : 0;
     // the segment's tiles: [a, a + len) of the unit, wrapped at kt
     const int a = g.tile(g.kb), len = g.ke - g.kb;
     const int first_end = a + len < g.kt ? a + len : g.kt;
@@ -588,7 +704,7 @@ __device__ void metadata(Smem& s, const AttnParams& p, SegIter iter) {
       const int t0 = part == 0 ? a : 0, t1 = part == 0 ? first_end : a + len - g.kt;
       int pg1 = t1 * kPagesPerTile;
       if (pg1 > npg) pg1 = npg;
-      if (pg1 > p.max_pages) pg1 = p.max_pages;
+      if (pg1 > g.pages) pg1 = g.pages;
       for (int pg = t0 * kPagesPerTile + lane; pg < pg1; pg += 4 * 32) {
         int v[4];
 #pragma unroll
@@ -713,8 +829,9 @@ __device__ bool build_ancestors(Smem& s, const AttnParams& p, const Seg& g) {
 
 // A warp whose wait gives up (ok = false) keeps walking the segments with its work skipped, so that the
 // ancestor build's named barriers are still reached by all 256 softmax threads; it reports the abort once.
-template <bool kFp8>
-__device__ void softmax_epilogue(Smem& s, const AttnParams& p, SegIter iter, uint32_t tmem, int qt) {
+template <class M>
+__device__ void softmax_epilogue(Smem& s, const typename M::Params& p, SegIter<M> iter, uint32_t tmem, int qt) {
+  constexpr bool kFp8 = M::kFp8;
   const int r = threadIdx.x - 128 - qt * kBM;  // row of M tile qt == TMEM lane
   const int wq = (threadIdx.x >> 5) & 3;
   const uint32_t lane_base = tmem + (static_cast<uint32_t>(wq * 32) << 16);
@@ -730,10 +847,12 @@ __device__ void softmax_epilogue(Smem& s, const AttnParams& p, SegIter iter, uin
     const int buf = sidx & 1;
     const int node = (g.mp * kAttnQTiles + qt) * nodes_per_tile + r / p.group;
     const int head = g.kvh * p.group + (r % p.group);
-    const bool row_valid = node < g.N;
+    const bool row_valid = node < g.rows;
     // the segment reads a tile with tree keys (tiles P / kBN .. kt - 1) iff its rotated range reaches P / kBN
-    if (g.tile(g.kb) + (g.ke - g.kb) > g.P / kBN && !build_ancestors(s, p, g)) ok = false;
-    const uint32_t* anc = &s.anc[row_valid ? node : 0][0];
+    // (a group item has no tree keys, and more rows than there are bitsets)
+    const bool group_item = M::kShared && g.N == 0;
+    if (!group_item && g.tile(g.kb) + (g.ke - g.kb) > g.P / kBN && !build_ancestors(s, p, g)) ok = false;
+    const uint32_t* anc = &s.anc[row_valid && !group_item ? node : 0][0];
     float m_use = -INFINITY, l = 0.f;
     for (int t = g.kb; t < g.ke; ++t, ++it) {
       const int kv = g.tile(t);
@@ -847,6 +966,40 @@ __device__ void softmax_epilogue(Smem& s, const AttnParams& p, SegIter iter, uin
     tc_fence_after();
     mbar_arrive(&s.bar_metaempty[buf]);
     const bool split = g.c0 != g.c1;
+    if constexpr (M::kShared) {
+      // the row's state (unnormalised O, m, l): a whole unit's into the row's own place, a part of a unit's into
+      // this CTA's slot; the unit's first CTA leaves word where the row's state is
+      const int kind = group_item ? 1 : 0;
+      const int li = (g.off + node) * p.group + r % p.group;  // row among those of the kv head
+      const int myslot = g.slot * kAttnQTiles + qt;
+#pragma unroll
+      for (int cc = 0; cc < 128; cc += 32) {
+        uint32_t o[32];
+        tmem_ld32(lane_base + o_col + cc, o);
+        tmem_ld_wait();
+        if (!row_valid) continue;
+#pragma unroll
+        for (int c = 0; c < 32; c += 4)
+          __stcg(split ? part_ptr(p, myslot, (cc + c) >> 2, r) : p.row_o(kind, g.kvh, (cc + c) >> 2) + li,
+                 make_float4(__uint_as_float(o[c]), __uint_as_float(o[c + 1]), __uint_as_float(o[c + 2]),
+                             __uint_as_float(o[c + 3])));
+      }
+      if (row_valid) {
+        if (split) {
+          __stcg(&p.part_ml[static_cast<long long>(myslot) * kBM + r], make_float2(m_use, l));
+          __stcg(&p.part_ok[static_cast<long long>(myslot) * kBM + r], seg_ok ? 1 : 0);
+        } else {
+          __stcg(p.row_ml(kind, g.kvh) + li, make_float2(m_use, l));
+        }
+        if (!split || static_cast<int>(blockIdx.x) == g.c0) {
+          const int shares = !group_item && s.item_x[g.b] > 0 ? kRowShares : 0;
+          const int how = split ? kRowSplit : (seg_ok ? kRowWhole : kRowBad);
+          __stcg(p.row_at(kind, g.kvh) + li, make_int4(how | shares, g.c0, g.c1, qt * kBM + r));
+        }
+      }
+      ++sidx;
+      continue;
+    }
     const long long grow = static_cast<long long>(g.off + node) * p.hq + head;  // global row
     if (!split) {
       const float inv_l = p.v_scale / l;  // the V cache's scale (1 for a bf16 cache)
@@ -888,13 +1041,14 @@ __device__ void softmax_epilogue(Smem& s, const AttnParams& p, SegIter iter, uin
     }
     ++sidx;
   }
-  if (!ok) set_abort(s, p);
+  if (!ok) set_abort<M>(s, p);
 }
 
-template <bool kFp8>
+template <class M>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                          const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
+                          const __grid_constant__ CUtensorMap tm_v, const typename M::Params p) {
+  constexpr bool kFp8 = M::kFp8;
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -945,38 +1099,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // Slot blockIdx.x of the split-unit table is written only by this CTA (if it starts a split unit);
   // clear what an earlier call left there.
-  if (tid == 0 && blockIdx.x < kMaxGrid) p.units[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if constexpr (M::kShared) {
+    if (tid == 0) __stcg(&p.cta_ok[blockIdx.x], 1);  // taken back below if this CTA gives up
+  } else {
+    if (tid == 0 && blockIdx.x < kMaxGrid) p.units[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
 #ifdef JF_DEBUG
   if (tid == 0 && *reinterpret_cast<volatile int*>(&g_debug_hold) != 0) {
     const uint64_t t0 = globaltimer();
     while (*reinterpret_cast<volatile int*>(&g_debug_hold) != 0) {
       if (globaltimer() - t0 > kWaitLimitNs) {
-        set_abort(s, p);
+        set_abort<M>(s, p);
         break;
       }
     }
   }
 #endif
-  build_plan(s, p);
+  int items = p.batch;
+  if constexpr (M::kShared) {
+    items = p.num_groups + p.batch;
+    build_shared_plan(s, p);
+    if (tid == 0 && s.bad_meta != 0) __stcg(&p.cta_ok[blockIdx.x], 0);
+  } else {
+    build_plan(s, p);
+  }
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   bool idle = s.bad_meta != 0 || s.abort_flag != 0;  // abort_flag: set above by the debug build only
   if (idle && blockIdx.x == 0 && tid == 0) report(p.status, JF_ERR_DEVICE_CHECK);
-  const long long W = s.cum_work[p.batch];
+  const long long W = s.cum_work[items];
   const int G = static_cast<int>(W < static_cast<long long>(gridDim.x) ? W : static_cast<long long>(gridDim.x));
   idle = idle || W <= 0 || static_cast<int>(blockIdx.x) >= G;
   if (idle) {  // uniform over the CTA
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
     return;
   }
-  SegIter iter;
+  SegIter<M> iter;
   iter.x = static_cast<long long>(blockIdx.x) * W / G;
   iter.xend = static_cast<long long>(blockIdx.x + 1) * W / G;
   iter.W = W;
   iter.G = G;
   {
     // first sequence touched by this CTA: binary search over cum_work
-    int lo = 0, hi = p.batch - 1;
+    int lo = 0, hi = items - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (s.cum_work[mid] <= iter.x) lo = mid; else hi = mid - 1;
@@ -993,16 +1158,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;\n" ::: "memory");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::: "memory");
     if (warp == 0 || warp == 2) {
-      kv_producer<kFp8>(s, p, iter, warp == 2, &tm_q, warp == 2 ? &tm_v : &tm_k);
+      kv_producer<M>(s, p, iter, warp == 2, &tm_q, warp == 2 ? &tm_v : &tm_k);
     } else if (warp == 1) {
-      mma_issuer<kFp8>(s, p, iter, tmem);
+      mma_issuer<M>(s, p, iter, tmem);
     } else {
-      metadata(s, p, iter);
+      metadata<M>(s, p, iter);
     }
   } else {
     if (kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n" ::: "memory");
-    softmax_epilogue<kFp8>(s, p, iter, tmem, warp < 8 ? 0 : 1);
+    softmax_epilogue<M>(s, p, iter, tmem, warp < 8 ? 0 : 1);
   }
   tc_fence_before();
   __syncthreads();
@@ -1134,34 +1299,116 @@ __global__ void __launch_bounds__(kCombineThreads, 2) combine_kernel(const AttnP
   }
 }
 
+// ------------------------------------------------------------------------------------------------
+// Shared prefix: joins every row's two states, each whole or in the parts of a split unit, and stores the output.  A
+// block takes 32 rows of one kv head (one per lane); its warps take 16 columns each.
+// ------------------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(kCombineThreads, 2) shared_combine_kernel(const SharedAttnParams p, int ncta) {
+  static_assert(4 * kCombineQuads * (kCombineThreads / 32) == 128, "a block covers the columns");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention grid has completed
+  const int tid = threadIdx.x, lane = tid & 31, q0 = (tid >> 5) * kCombineQuads;
+  if (__syncthreads_or(tid < ncta && __ldcg(&p.cta_ok[tid]) == 0)) return;
+  const long long rows = p.rows();
+  const int blocks = static_cast<int>((rows + 31) / 32);
+  for (long long item = blockIdx.x; item < static_cast<long long>(blocks) * p.hkv; item += gridDim.x) {
+    const int kvh = static_cast<int>(item / blocks);
+    const long long li = (item % blocks) * 32 + lane;
+    if (li >= rows) continue;
+    float M = -INFINITY, L = 0.f;
+    float4 acc[kCombineQuads];
+#pragma unroll
+    for (int q = 0; q < kCombineQuads; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float2 ml, const float4 (&v)[kCombineQuads]) {
+      if (ml.x == -INFINITY) return;
+      const float top = fmaxf(M, ml.x);
+      const float a = ex2_approx(M - top), w = ex2_approx(ml.x - top);
+      L = fmaf(w, ml.y, L * a);
+#pragma unroll
+      for (int q = 0; q < kCombineQuads; ++q) {
+        acc[q].x = fmaf(w, v[q].x, acc[q].x * a);
+        acc[q].y = fmaf(w, v[q].y, acc[q].y * a);
+        acc[q].z = fmaf(w, v[q].z, acc[q].z * a);
+        acc[q].w = fmaf(w, v[q].w, acc[q].w * a);
+      }
+      M = top;
+    };
+    bool ok = true, shares = false;
+    for (int kind = 0; kind < 2; ++kind) {
+      if (kind == 1 && !shares) break;
+      const int4 at = __ldcg(p.row_at(kind, kvh) + li);
+      if (kind == 0) shares = (at.x & kRowShares) != 0;
+      const int how = at.x & ~kRowShares;
+      float4 v[kCombineQuads];
+      if (how == kRowWhole) {
+#pragma unroll
+        for (int q = 0; q < kCombineQuads; ++q) v[q] = __ldcg(p.row_o(kind, kvh, q0 + q) + li);
+        add(__ldcg(p.row_ml(kind, kvh) + li), v);
+      } else if (how == kRowSplit) {
+        const int qt = at.w / kBM, r = at.w % kBM;
+        for (int c = at.y; c <= at.z; ++c) {
+          const int sl = slot_of(c, at.y) * kAttnQTiles + qt;
+#pragma unroll
+          for (int q = 0; q < kCombineQuads; ++q) v[q] = __ldcg(part_ptr(p, sl, q0 + q, r));
+          ok = ok && __ldcg(&p.part_ok[static_cast<long long>(sl) * kBM + r]) != 0;
+          add(__ldcg(&p.part_ml[static_cast<long long>(sl) * kBM + r]), v);
+        }
+      } else {
+        ok = false;
+      }
+    }
+    if (!ok) continue;
+    const long long grow = li / p.group * p.hq + kvh * p.group + li % p.group;
+    const float inv = p.v_scale / L;  // the V cache's scale (1 for a bf16 cache)
+    uint2* dst = reinterpret_cast<uint2*>(p.out + grow * 128 + q0 * 4);
+#pragma unroll
+    for (int q = 0; q < kCombineQuads; ++q)
+      dst[q] = make_uint2(pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv));
+    if (q0 == 0 && p.lse != nullptr) p.lse[grow] = (M + __log2f(L)) * 0.69314718055994531f;
+  }
+}
+
 }  // namespace attn
 
 static_assert(sizeof(attn::Smem) + 1024 <= 227 * 1024, "shared memory of one CTA (plus alignment slack)");
 size_t attention_smem_bytes() { return sizeof(attn::Smem) + 1024; }
 
-cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                  const AttnParams& p, int grid, bool fp8_cache, cudaStream_t stream) {
+// Sets the kernel's attributes the first time it is launched on a device, then launches it.
+template <class M>
+static cudaError_t launch_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                    const typename M::Params& p, int grid, cudaStream_t stream) {
   static std::atomic<bool> attr_set[kMaxDevices];
   const int dev = current_device();
   if (dev < 0) return cudaErrorInvalidDevice;
   const size_t smem = attention_smem_bytes();
   if (!attr_set[dev].load(std::memory_order_acquire)) {
-    cudaError_t e = cudaFuncSetAttribute(attn::tree_attention_kernel<false>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(attn::tree_attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
+    const cudaError_t e = cudaFuncSetAttribute(attn::tree_attention_kernel<M>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  cudaError_t e = fp8_cache ? launch_pdl(attn::tree_attention_kernel<true>, dim3(grid), dim3(attn::kThreads), smem,
-                                         stream, nullptr, tm_q, tm_k, tm_v, p)
-                            : launch_pdl(attn::tree_attention_kernel<false>, dim3(grid), dim3(attn::kThreads), smem,
-                                         stream, nullptr, tm_q, tm_k, tm_v, p);
+  return launch_pdl(attn::tree_attention_kernel<M>, dim3(grid), dim3(attn::kThreads), smem, stream, nullptr, tm_q, tm_k,
+                    tm_v, p);
+}
+
+cudaError_t launch_tree_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                  const AttnParams& p, int grid, bool fp8_cache, cudaStream_t stream) {
+  const cudaError_t e = fp8_cache
+                            ? launch_attention<attn::Mode<true, false>>(tm_q, tm_k, tm_v, p, grid, stream)
+                            : launch_attention<attn::Mode<false, false>>(tm_q, tm_k, tm_v, p, grid, stream);
   if (e != cudaSuccess) return e;
   // The combine kernel may start as soon as the attention grid is scheduled; its griddepcontrol.wait
   // holds it until the attention grid has finished and its writes are visible.
   return launch_pdl(attn::combine_kernel, dim3(2 * grid), dim3(attn::kCombineThreads), 0, stream, nullptr, p, grid);
+}
+
+cudaError_t launch_tree_attention_shared(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                         const SharedAttnParams& p, int grid, bool fp8_cache, cudaStream_t stream) {
+  const cudaError_t e = fp8_cache ? launch_attention<attn::Mode<true, true>>(tm_q, tm_k, tm_v, p, grid, stream)
+                                  : launch_attention<attn::Mode<false, true>>(tm_q, tm_k, tm_v, p, grid, stream);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn::shared_combine_kernel, dim3(2 * grid), dim3(attn::kCombineThreads), 0, stream, nullptr, p,
+                    grid);
 }
 
 }  // namespace jf
