@@ -3,7 +3,8 @@
 //
 // Design: the walk is a chain of dependent draws, so latency matters.  One cluster per sequence; each step brings the
 // current node's row into the cluster's shared memory and draws from it (sampling.cuh); every CTA knows the token drawn
-// and finds the same child in its own copy of the tree.
+// and finds the same child in its own copy of the tree.  While a row is drawn from, the rows of the node's first children,
+// the only candidates for the next step, are prefetched into L2.
 #include "sampling.cuh"
 
 namespace jf {
@@ -12,12 +13,14 @@ namespace smp {
 struct Tree {
   int tok[kMaxAcceptNodes], par[kMaxAcceptNodes];
   int kid[2];  // the child found, by step parity
+  int ahead;   // rows prefetched in this step
 };
+constexpr int kAhead = 8;  // a tree's nodes rarely have more children than the eight candidates they are built from
 constexpr size_t kTreeOff = kSliceOff;
 constexpr size_t kWalkSliceOff = (kTreeOff + sizeof(Tree) + 127) & ~size_t(127);
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     accept_sampled_kernel(const int32_t* __restrict__ token, const int32_t* __restrict__ parent,
                           const T* __restrict__ logits, const float* __restrict__ u, const SampleParams sp,
                           int num_nodes, int vocab, int max_depth, int32_t* __restrict__ accepted_len,
@@ -32,11 +35,6 @@ __global__ void __launch_bounds__(kThreads)
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const long long b = blockIdx.x / C;
   const int tid = threadIdx.x;
-  if (tid == 0) {
-    mbar_init(&s.bar, 1);
-    fence_barrier_init();
-  }
-  if (tid < 128) s.tab[tid] = g_exp2_frac128[tid];
   Row<T> row(s, raw + kWalkSliceOff, rank, C, vocab);
   cluster.sync();  // every CTA of the cluster runs (remote shared memory may be written); the barrier is initialised
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before this one has completed
@@ -63,11 +61,17 @@ __global__ void __launch_bounds__(kThreads)
       if (rank == 0 && tid == 0) report(status, JF_ERR_DEVICE_CHECK);
       return;  // between two draws no CTA writes into another's shared memory
     }
-    if (tid == 0) t.kid[step & 1] = INT_MAX;
+    if (tid == 0) {
+      t.kid[step & 1] = INT_MAX;
+      t.ahead = 0;
+    }
     fence_proxy_async_smem();
     __syncthreads();  // the previous row's last reads are done before the copy of this one starts
     row.start(rows + static_cast<long long>(cur) * vocab);
-    const Drawn d = row.draw(rp, us, step & 1);
+    if (L < max_depth)
+      for (int c = tid; c < num_nodes; c += kThreads)
+        if (t.par[c] == cur && atomicAdd(&t.ahead, 1) < kAhead) row.prefetch(rows + static_cast<long long>(c) * vocab);
+    const Drawn d = row.template draw<true>(rp, us, step & 1);
     if (!d.ok) {
       volatile int never = 0;
       mbar_wait(&s.bar, step & 1, &never);  // no copy of this CTA is left in flight
@@ -105,19 +109,10 @@ cudaError_t launch_walk(const int32_t* token, const int32_t* parent, const T* lo
                         const SampleParams& sp, int batch, int num_nodes, int vocab, int max_depth,
                         int32_t* accepted_len, int32_t* path, int32_t* bonus, float* logprob, int32_t* status,
                         cudaStream_t stream) {
-  static std::atomic<bool> attr_set[kMaxDevices];
-  const int dev = current_device();
-  if (dev < 0) return cudaErrorInvalidDevice;
-  if (!attr_set[dev].load(std::memory_order_acquire)) {
-    cudaError_t e = cudaFuncSetAttribute(accept_sampled_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(accept_sampled_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem);
-    if (e != cudaSuccess) return e;
-    attr_set[dev].store(true, std::memory_order_release);
-  }
-  // the widest cluster that leaves every CTA a slice worth its threads
-  int cluster = 1;
-  while (cluster < kMaxCluster && slice_len(vocab, cluster) > 2 * kThreads) cluster *= 2;
+  static std::atomic<int> sms_of[kMaxDevices];
+  const int sms = prepare_kernel(accept_sampled_kernel<T>, sms_of);
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const int cluster = cluster_size(batch, vocab, sizeof(T), sms);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cluster;

@@ -8,7 +8,7 @@ namespace jf {
 namespace smp {
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     sample_kernel(const T* __restrict__ logits, long long row_stride, int vocab, const float* __restrict__ u,
                   const SampleParams sp, int32_t* __restrict__ token, float* __restrict__ logprob, int32_t* status) {
   extern __shared__ __align__(128) uint8_t raw[];
@@ -17,11 +17,6 @@ __global__ void __launch_bounds__(kThreads)
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const long long r = blockIdx.x / C;
   const int tid = threadIdx.x;
-  if (tid == 0) {
-    mbar_init(&s.bar, 1);
-    fence_barrier_init();
-  }
-  if (tid < 128) s.tab[tid] = g_exp2_frac128[tid];
   Row<T> row(s, raw + kSliceOff, rank, C, vocab);
   cluster.sync();  // every CTA of the cluster runs (remote shared memory may be written); the barrier is initialised
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the logits come from the kernel before this one
@@ -33,38 +28,26 @@ __global__ void __launch_bounds__(kThreads)
     return;
   }
   row.start(logits + r * row_stride);
-  const Drawn d = row.draw(rp, ur, 0);
+  const Drawn d = row.template draw<false>(rp, ur, 0);
   if (!d.ok) {
     volatile int never = 0;
     mbar_wait(&s.bar, 0, &never);  // no copy of this CTA is left in flight
     if (rank == 0 && tid == 0) report(status, JF_ERR_TIMEOUT);
     return;
   }
-  if (rank == 0 && tid == 0) {
+  if (d.mine) {
     token[r] = d.token;
     if (logprob != nullptr) logprob[r] = d.logprob;
   }
 }
 
-// Smallest cluster whose CTAs hold their slice in kSliceGoal bytes, so that several CTAs share an SM and one row's
-// copies run under another's passes; 16 beyond that.
-constexpr size_t kSliceGoal = 80 * 1024;
-
 template <typename T>
 cudaError_t launch(const T* logits, long long row_stride, int rows, int vocab, const float* u, const SampleParams& sp,
                    int32_t* token, float* logprob, int32_t* status, cudaStream_t stream) {
-  static std::atomic<bool> attr_set[kMaxDevices];
-  const int dev = current_device();
-  if (dev < 0) return cudaErrorInvalidDevice;
-  if (!attr_set[dev].load(std::memory_order_acquire)) {
-    cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem);
-    if (e != cudaSuccess) return e;
-    attr_set[dev].store(true, std::memory_order_release);
-  }
-  int cluster = 1;
-  while (cluster < kMaxCluster && slice_bytes(vocab, cluster, sizeof(T)) > kSliceGoal) cluster *= 2;
+  static std::atomic<int> sms_of[kMaxDevices];
+  const int sms = prepare_kernel(sample_kernel<T>, sms_of);
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const int cluster = cluster_size(rows, vocab, sizeof(T), sms);
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cluster;
