@@ -19,8 +19,8 @@ constexpr int kAhead = 8;  // a tree's nodes rarely have more children than the 
 constexpr size_t kTreeOff = kSliceOff;
 constexpr size_t kWalkSliceOff = (kTreeOff + sizeof(Tree) + 127) & ~size_t(127);
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, bool kResident>
+__global__ void __launch_bounds__(kThreads)
     accept_sampled_kernel(const int32_t* __restrict__ token, const int32_t* __restrict__ parent,
                           const T* __restrict__ logits, const float* __restrict__ u, const SampleParams sp,
                           int num_nodes, int vocab, int max_depth, int32_t* __restrict__ accepted_len,
@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const long long b = blockIdx.x / C;
   const int tid = threadIdx.x;
-  Row<T> row(s, raw + kWalkSliceOff, rank, C, vocab);
+  Row<T, kResident> row(s, raw + kWalkSliceOff, rank, C, vocab);
   cluster.sync();  // every CTA of the cluster runs (remote shared memory may be written); the barrier is initialised
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before this one has completed
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -48,8 +48,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     t.tok[i] = __ldg(token + b * num_nodes + i);
     bad = bad || pi < -1 || pi >= i;
   }
-  RowParams rp;
-  bad = __syncthreads_or(bad) || !read_params(sp, b, rp);  // the same in every CTA of the cluster
+  if (tid == kThreads - 1) s.rp = read_params(sp, b, 0.f);
+  bad = __syncthreads_or(bad) || !s.rp.ok;  // the same in every CTA of the cluster
   if (bad) {
     if (rank == 0 && tid == 0) report(status, JF_ERR_DEVICE_CHECK);
     return;
@@ -57,11 +57,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   int cur = 0, L = 0, drawn = -1;
   for (int step = 0;; ++step) {
     const float us = __ldg(ub + step);  // step == L <= max_depth
-    if (!good_u(us)) {
+    if (!(us >= 0.f && us < 1.f)) {
       if (rank == 0 && tid == 0) report(status, JF_ERR_DEVICE_CHECK);
       return;  // between two draws no CTA writes into another's shared memory
     }
     if (tid == 0) {
+      s.rp.u = us;
       t.kid[step & 1] = INT_MAX;
       t.ahead = 0;
     }
@@ -71,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (L < max_depth)
       for (int c = tid; c < num_nodes; c += kThreads)
         if (t.par[c] == cur && atomicAdd(&t.ahead, 1) < kAhead) row.prefetch(rows + static_cast<long long>(c) * vocab);
-    const Drawn d = row.template draw<true>(rp, us, step & 1);
+    const Drawn d = row.template draw<true>(step & 1);
     if (!d.ok) {
       volatile int never = 0;
       mbar_wait(&s.bar, step & 1, &never);  // no copy of this CTA is left in flight
@@ -104,23 +105,39 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-template <typename T>
-cudaError_t launch_walk(const int32_t* token, const int32_t* parent, const T* logits, const float* u,
-                        const SampleParams& sp, int batch, int num_nodes, int vocab, int max_depth,
+template <typename T, bool kResident>
+cudaError_t launch_walk(int cluster, size_t smem, const int32_t* token, const int32_t* parent, const T* logits,
+                        const float* u, const SampleParams& sp, int batch, int num_nodes, int vocab, int max_depth,
                         int32_t* accepted_len, int32_t* path, int32_t* bonus, float* logprob, int32_t* status,
                         cudaStream_t stream) {
-  static std::atomic<int> sms_of[kMaxDevices];
-  const int sms = prepare_kernel(accept_sampled_kernel<T>, sms_of);
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  const int cluster = cluster_size(batch, vocab, sizeof(T), sms);
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = prepare_kernel(accept_sampled_kernel<T, kResident>, done);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cluster;
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
-  return launch_pdl(accept_sampled_kernel<T>, dim3(static_cast<unsigned>(batch) * cluster), dim3(kThreads),
-                    kWalkSliceOff + slice_bytes(vocab, cluster, sizeof(T)), stream, &attr, token, parent, logits, u, sp,
-                    num_nodes, vocab, max_depth, accepted_len, path, bonus, logprob, status);
+  return launch_pdl(accept_sampled_kernel<T, kResident>, dim3(static_cast<unsigned>(batch) * cluster), dim3(kThreads),
+                    smem, stream, &attr, token, parent, logits, u, sp, num_nodes, vocab, max_depth, accepted_len, path,
+                    bonus, logprob, status);
+}
+
+// The slices stay in shared memory where they fit.
+template <typename T>
+cudaError_t choose_walk(const int32_t* token, const int32_t* parent, const T* logits, const float* u,
+                        const SampleParams& sp, int batch, int num_nodes, int vocab, int max_depth,
+                        int32_t* accepted_len, int32_t* path, int32_t* bonus, float* logprob, int32_t* status,
+                        cudaStream_t stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const int c = widest_cluster(batch, vocab, sms);
+  const size_t smem = kWalkSliceOff + slice_bytes(vocab, c, sizeof(T));
+  if (smem <= kMaxDynSmem)
+    return launch_walk<T, true>(c, smem, token, parent, logits, u, sp, batch, num_nodes, vocab, max_depth, accepted_len,
+                                path, bonus, logprob, status, stream);
+  return launch_walk<T, false>(c, kWalkSliceOff, token, parent, logits, u, sp, batch, num_nodes, vocab, max_depth,
+                               accepted_len, path, bonus, logprob, status, stream);
 }
 
 }  // namespace smp
@@ -129,9 +146,9 @@ cudaError_t launch_accept_sampled(const int32_t* token, const int32_t* parent, c
                                   const float* u, const SampleParams& sp, int batch, int num_nodes, int vocab,
                                   int max_depth, int32_t* accepted_len, int32_t* path, int32_t* bonus, float* logprob,
                                   int32_t* status, cudaStream_t stream) {
-  return bf16 ? smp::launch_walk(token, parent, static_cast<const __nv_bfloat16*>(logits), u, sp, batch, num_nodes,
+  return bf16 ? smp::choose_walk(token, parent, static_cast<const __nv_bfloat16*>(logits), u, sp, batch, num_nodes,
                                  vocab, max_depth, accepted_len, path, bonus, logprob, status, stream)
-              : smp::launch_walk(token, parent, static_cast<const float*>(logits), u, sp, batch, num_nodes, vocab,
+              : smp::choose_walk(token, parent, static_cast<const float*>(logits), u, sp, batch, num_nodes, vocab,
                                  max_depth, accepted_len, path, bonus, logprob, status, stream);
 }
 

@@ -1,13 +1,14 @@
 // sample.cu -- jf_sample: one token per row of logits (sm_100a, SIMT + clusters).
 //
-// Design: one thread-block cluster per row.  The row is read from memory once, by bulk copies into the shared memory
-// of the cluster's CTAs, and every pass of the draw (sampling.cuh) then reads it there.
+// Design: a thread-block cluster takes a row.  While few rows are asked for, its CTAs hold the row in shared memory, so
+// that each pass of the draw (sampling.cuh) is short; with many rows the barriers of wide clusters would dominate, and
+// narrow clusters, down to one CTA a row, read the row again from L2 in each pass.
 #include "sampling.cuh"
 
 namespace jf {
 namespace smp {
 
-template <typename T>
+template <typename T, bool kResident>
 __global__ void __launch_bounds__(kThreads, 2)
     sample_kernel(const T* __restrict__ logits, long long row_stride, int vocab, const float* __restrict__ u,
                   const SampleParams sp, int32_t* __restrict__ token, float* __restrict__ logprob, int32_t* status) {
@@ -17,22 +18,21 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const long long r = blockIdx.x / C;
   const int tid = threadIdx.x;
-  Row<T> row(s, raw + kSliceOff, rank, C, vocab);
+  Row<T, kResident> row(s, raw + kSliceOff, rank, C, vocab);
   cluster.sync();  // every CTA of the cluster runs (remote shared memory may be written); the barrier is initialised
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the logits come from the kernel before this one
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  RowParams rp;
-  const float ur = __ldg(u + r);
-  if (!read_params(sp, r, rp) || !good_u(ur)) {  // the same in every CTA of the cluster
-    if (rank == 0 && tid == 0) report(status, JF_ERR_DEVICE_CHECK);
-    return;
-  }
   row.start(logits + r * row_stride);
-  const Drawn d = row.template draw<false>(rp, ur, 0);
+  if (tid == kThreads - 1) s.rp = read_params(sp, r, __ldg(u + r));
+  const Drawn d = row.template draw<false>(0);
   if (!d.ok) {
     volatile int never = 0;
     mbar_wait(&s.bar, 0, &never);  // no copy of this CTA is left in flight
     if (rank == 0 && tid == 0) report(status, JF_ERR_TIMEOUT);
+    return;
+  }
+  if (!s.rp.ok) {  // the same in every CTA of the cluster
+    if (rank == 0 && tid == 0) report(status, JF_ERR_DEVICE_CHECK);
     return;
   }
   if (d.mine) {
@@ -41,21 +41,33 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-template <typename T>
-cudaError_t launch(const T* logits, long long row_stride, int rows, int vocab, const float* u, const SampleParams& sp,
-                   int32_t* token, float* logprob, int32_t* status, cudaStream_t stream) {
-  static std::atomic<int> sms_of[kMaxDevices];
-  const int sms = prepare_kernel(sample_kernel<T>, sms_of);
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  const int cluster = cluster_size(rows, vocab, sizeof(T), sms);
+template <typename T, bool kResident>
+cudaError_t launch(int cluster, size_t smem, const T* logits, long long row_stride, int rows, int vocab, const float* u,
+                   const SampleParams& sp, int32_t* token, float* logprob, int32_t* status, cudaStream_t stream) {
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = prepare_kernel(sample_kernel<T, kResident>, done);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cluster;
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
-  return launch_pdl(sample_kernel<T>, dim3(static_cast<unsigned>(rows) * cluster), dim3(kThreads),
-                    kSliceOff + slice_bytes(vocab, cluster, sizeof(T)), stream, &attr, logits, row_stride, vocab, u, sp,
-                    token, logprob, status);
+  return launch_pdl(sample_kernel<T, kResident>, dim3(static_cast<unsigned>(rows) * cluster), dim3(kThreads), smem,
+                    stream, &attr, logits, row_stride, vocab, u, sp, token, logprob, status);
+}
+
+template <typename T>
+cudaError_t choose(const T* logits, long long row_stride, int rows, int vocab, const float* u, const SampleParams& sp,
+                   int32_t* token, float* logprob, int32_t* status, cudaStream_t stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  int c = widest_cluster(rows, vocab, sms);
+  const size_t smem = kSliceOff + slice_bytes(vocab, c, sizeof(T));
+  if (smem <= (rows * static_cast<long long>(c) <= sms ? kMaxDynSmem : kTwoPerSm))
+    return launch<T, true>(c, smem, logits, row_stride, rows, vocab, u, sp, token, logprob, status, stream);
+  // slices that do not fit: two CTAs an SM
+  while (c < kMaxCluster && rows * 2ll * c <= 2 * sms && slice_len(vocab, c) > kMinSlice) c *= 2;
+  return launch<T, false>(c, kSliceOff, logits, row_stride, rows, vocab, u, sp, token, logprob, status, stream);
 }
 
 }  // namespace smp
@@ -63,9 +75,9 @@ cudaError_t launch(const T* logits, long long row_stride, int rows, int vocab, c
 cudaError_t launch_sample(const void* logits, bool bf16, long long row_stride, int rows, int vocab, const float* u,
                           const SampleParams& sp, int32_t* token, float* logprob, int32_t* status,
                           cudaStream_t stream) {
-  return bf16 ? smp::launch(static_cast<const __nv_bfloat16*>(logits), row_stride, rows, vocab, u, sp, token, logprob,
+  return bf16 ? smp::choose(static_cast<const __nv_bfloat16*>(logits), row_stride, rows, vocab, u, sp, token, logprob,
                             status, stream)
-              : smp::launch(static_cast<const float*>(logits), row_stride, rows, vocab, u, sp, token, logprob, status,
+              : smp::choose(static_cast<const float*>(logits), row_stride, rows, vocab, u, sp, token, logprob, status,
                             stream);
 }
 
