@@ -72,6 +72,16 @@ def test_single_tokens(fp8, B, shared, suffix):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_few_rows_at_the_edges_of_their_kernel(fp8):
+    # 16 and 17 rows, 1024 and 1025 own keys (nodes included), the last page full, begun and empty but for one slot
+    suffix = [1023, 1024, 1008 - 3, 15, 0, 14, 1019, 1000]
+    nodes = [1, 1, 3, 1, 4, 2, 4, 5]
+    check(shared_inputs(40, 8, 2, [(5, 48), (3, 33)], nodes, suffix), fp8)
+    check(shared_inputs(41, 16, 1, [(2, 0), (6, 160)], [1] * 8, suffix), fp8)
+    check(shared_inputs(42, 2, 2, [(8, 7)], [16, 17, 1, 15, 0, 16, 2, 16], suffix), fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_large_trees_ragged_groups_and_empty_sequences(fp8):
     nodes = [256, 0, 1, 255, 130, 0, 17, 64, 0]
     suffix = [0, 5, 130, 16, 1, 0, 333, 48, 7]

@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libjf.so")
 DEBUG_LIB = os.path.join(PKG, "libjf_debug.so")
 SOURCES = ["jf_api.cu", "tree_attention.cu", "build_tree.cu", "frontier.cu", "accept.cu", "commit_kv.cu",
-           "kv_append.cu", "serving_api.cu", "sample.cu", "accept_sampled.cu"]
+           "kv_append.cu", "serving_api.cu", "sample.cu", "accept_sampled.cu", "shared_small.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

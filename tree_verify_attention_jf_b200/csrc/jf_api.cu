@@ -144,10 +144,13 @@ jf_status attention_call(const void* q, const void* k_cache, const void* v_cache
   p.group_offsets = shared->group_offsets;
   p.shared_lens = shared->shared_lens;
   p.num_groups = shared->num_groups;
+  // worth a launch of its own when sequences of few rows are the rule
+  p.small = static_cast<long long>(total_nodes) * group <= 2ll * kSmallRows * batch ? 1 : 0;
   p.cta_ok = reinterpret_cast<int32_t*>(ws + sw.ok_off);
   p.rows_o = reinterpret_cast<float4*>(ws + sw.o_off);
   p.rows_ml = reinterpret_cast<float2*>(ws + sw.ml_off);
   p.rows_at = reinterpret_cast<int4*>(ws + sw.at_off);
+  if (p.small && launch_shared_small(q, k_cache, v_cache, p, fp8, st) != cudaSuccess) return JF_ERR_CUDA;
   return launch_tree_attention_shared(tm_q, tm_k, tm_v, p, grid, fp8, st) == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 

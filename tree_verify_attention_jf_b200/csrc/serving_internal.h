@@ -29,10 +29,17 @@ cudaError_t launch_accept_sampled(const int32_t* token, const int32_t* parent, c
 // ---- tree attention over a shared prefix
 enum RowState : int { kRowBad = 0, kRowWhole = 1, kRowSplit = 2, kRowShares = 4 };
 
+// Sequences whose own keys a kernel of their own takes (shared_small.cu): few rows and few keys.
+constexpr int kSmallRows = 16, kSmallKeys = 1024;
+__host__ __device__ inline bool small_sequence(int nodes, int group, int keys) {
+  return nodes * group <= kSmallRows && keys <= kSmallKeys;
+}
+
 struct SharedAttnParams : AttnParams {
   const int32_t* group_offsets;  // [num_groups + 1] sequences
   const int32_t* shared_lens;    // [num_groups]
   int num_groups;
+  int small;        // whether that kernel runs
   int32_t* cta_ok;  // [kMaxGrid] 0 = the CTA gave up, or the batch's metadata are malformed
   // Softmax states of the rows, kind 0 from their own keys, kind 1 from the shared ones.  A row's place is
   // (node * group + head in the group) within its kv head, in which order an M tile's rows lie too.
@@ -80,6 +87,8 @@ jf_status attention_call(const void* q, const void* k_cache, const void* v_cache
                          float k_scale, float v_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
                          int32_t* dev_status, jf_stream_t stream);
 
+cudaError_t launch_shared_small(const void* q, const void* k_cache, const void* v_cache, const SharedAttnParams& p,
+                                bool fp8_cache, cudaStream_t stream);
 cudaError_t launch_tree_attention_shared(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                          const SharedAttnParams& p, int grid, bool fp8_cache, cudaStream_t stream);
 

@@ -300,7 +300,8 @@ __device__ void build_shared_plan(Smem& s, const SharedAttnParams& p) {
     s.item_x[G + b] = fits ? shared : -1;
     s.seq_p[G + b] = fits ? P - shared * kPage : 0;
     s.seq_off[G + b] = off;
-    s.item_n[G + b] = N;
+    // a small sequence's own keys are another kernel's work
+    s.item_n[G + b] = p.small && fits && N > 0 && small_sequence(N, p.group, P - shared * kPage + N) ? 0 : N;
   }
   if (bad) atomicOr(&s.bad_meta, 1);
   __syncthreads();
