@@ -83,17 +83,19 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ float s_o[kWarps][kRows][kHeadDim + 4];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ int s_parent[kRows];
+  __shared__ int s_page[(kSmallKeys + kPageSize - 1) / kPageSize];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kvh = blockIdx.x, b = blockIdx.y;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before this one (which may produce any input)
-  // the sequence; malformed offsets or lengths are left to the other kernel, which reports them
+  // the sequence; malformed offsets or lengths are left to the other kernel, which reports them.  (The loads that do not
+  // depend on the group go first.)
+  const int off = __ldg(p.tree_offsets + b), N = __ldg(p.tree_offsets + b + 1) - off, P = __ldg(p.prefix_lens + b);
   int lo = 0, hi = p.num_groups - 1;  // the last group that starts at or before b
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (__ldg(p.group_offsets + mid) <= b) lo = mid; else hi = mid - 1;
   }
-  const int off = __ldg(p.tree_offsets + b), N = __ldg(p.tree_offsets + b + 1) - off, P = __ldg(p.prefix_lens + b);
   const int len = __ldg(p.shared_lens + lo);
   if (off < 0 || N <= 0 || off > p.total_nodes - N || len < 0 || P < len) return;
   const int page0 = len / kPageSize, own = P - page0 * kPageSize;
@@ -101,24 +103,6 @@ __global__ void __launch_bounds__(kThreads)
   if (!small_sequence(N, p.group, own + N)) return;
   const int rows = N * p.group, keys = own + N, pages = (keys + kPageSize - 1) / kPageSize;
   const int32_t* bt = p.block_table + static_cast<long long>(b) * p.max_pages + page0;
-  // parents and page ids
-  bool bad = false;
-  if (tid < N) {
-    const int pi = __ldg(p.parent + off + tid);
-    bad = pi < -1 || pi >= tid;
-    s_parent[tid] = bad ? -1 : pi;
-  }
-  for (int i = tid; i < pages; i += kThreads) {
-    const int id = __ldg(bt + i);
-    bad = bad || id < 0 || id >= p.num_pages;
-  }
-  bad = __syncthreads_or(bad);
-  const long long li0 = static_cast<long long>(off) * p.group;  // the rows' place among those of the kv head
-  if (bad) {
-    if (tid == 0 && kvh == 0) report(p.status, JF_ERR_DEVICE_CHECK);
-    if (tid < rows) __stcg(p.row_at(0, kvh) + li0 + tid, make_int4(kRowBad, 0, 0, 0));
-    return;
-  }
   const int t = lane & 3, r0 = lane >> 2, r1 = r0 + 8;  // the quad's thread, and the rows of its fragments
   // Q: k-step kk contracts elements 32 t' + 4 kk .. + 3 of every quad thread t'
   uint32_t qa[8][4];
@@ -136,6 +120,25 @@ __global__ void __launch_bounds__(kThreads)
       qa[2 * i + 1][2 + half] = kFp8 ? f16_of_bf16(v.w) : v.w;
     }
   }
+  // parents and page ids
+  bool bad = false;
+  if (tid < N) {
+    const int pi = __ldg(p.parent + off + tid);
+    bad = pi < -1 || pi >= tid;
+    s_parent[tid] = bad ? -1 : pi;
+  }
+  for (int i = tid; i < pages; i += kThreads) {
+    const int id = __ldg(bt + i);
+    bad = bad || id < 0 || id >= p.num_pages;
+    s_page[i] = id;
+  }
+  bad = __syncthreads_or(bad);
+  const long long li0 = static_cast<long long>(off) * p.group;  // the rows' place among those of the kv head
+  if (bad) {
+    if (tid == 0 && kvh == 0) report(p.status, JF_ERR_DEVICE_CHECK);
+    if (tid < rows) __stcg(p.row_at(0, kvh) + li0 + tid, make_int4(kRowBad, 0, 0, 0));
+    return;
+  }
   // which of the (at most 16) tree nodes the two rows see: their root paths
   uint32_t sees[2] = {0, 0};
 #pragma unroll
@@ -151,29 +154,31 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   for (int pg = warp; pg < pages; pg += kWarps) {
-    const long long slot0 = static_cast<long long>(__ldg(bt + pg)) * kPageSize;
+    const long long slot0 = static_cast<long long>(s_page[pg]) * kPageSize;
     const int left = keys - pg * kPageSize;  // keys of this page that exist
     auto element = [&](int key) { return ((slot0 + key) * p.hkv + kvh) * kHeadDim; };
-    // S = Q K^T, keys 0-7 and 8-15: column (lane / 4) of each half is this thread's key
-    float s[2][4];
+    // K of keys 0-7 and 8-15: column (lane / 4) of each half is this thread's key.  V of keys 2 t, 2 t + 1, 2 t + 8 and
+    // 2 t + 9, dims 16 (lane / 4) .. + 15; all loads of the page are in flight together.
+    uint32_t kw[2][16], vw[4][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) load_row<kFp8, 32>(k_cache, element(8 * h + r0) + 32 * t, kw[h]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      load_row<kFp8, 16>(v_cache, element(2 * t + (i & 1) + 8 * (i >> 1)) + 16 * r0, vw[i]);
+    float s[2][4];  // S = Q K^T
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.f;
-      uint32_t kw[16];
-      load_row<kFp8, 32>(k_cache, element(8 * h + r0) + 32 * t, kw);
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) mma<kFp8>(s[h], qa[kk], kw[2 * kk], kw[2 * kk + 1]);
+      for (int kk = 0; kk < 8; ++kk) mma<kFp8>(s[h], qa[kk], kw[h][2 * kk], kw[h][2 * kk + 1]);
     }
-    // V rows of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9, dims 16 (lane / 4) .. + 15; rows that do not exist count as 0, so
-    // that what lies there cannot reach the output through 0 * V
-    uint32_t vw[4][8];
+    // V rows that do not exist count as 0, so that what lies there cannot reach the output through 0 * V
+    if (left < kPageSize) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int key = 2 * t + (i & 1) + 8 * (i >> 1);
-      load_row<kFp8, 16>(v_cache, element(key) + 16 * r0, vw[i]);
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (key >= left) vw[i][j] = 0;
+        for (int j = 0; j < 8; ++j)
+          if (2 * t + (i & 1) + 8 * (i >> 1) >= left) vw[i][j] = 0;
     }
     // mask, running max and sum per row (values 0, 1: row r0; 2, 3: row r1; keys 2 t, 2 t + 1 of each half)
     uint32_t pa[4];

@@ -1302,60 +1302,84 @@ __global__ void __launch_bounds__(kCombineThreads, 2) combine_kernel(const AttnP
 
 // ------------------------------------------------------------------------------------------------
 // Shared prefix: joins every row's two states, each whole or in the parts of a split unit, and stores the output.  A
-// block takes 32 rows of one kv head (one per lane); its warps take 16 columns each.
+// warp takes 32 rows of one kv head (one per lane) and 4 * kJoinQuads columns; a row's parts (the prefix of a few rows is
+// cut over up to all CTAs) are loaded kJoinBatch at a time.  Few rows are spread over four times the warps by narrow
+// columns, where many would read their descriptors four times for nothing (64 single tokens: 79 -> 74 us a call with
+// narrow columns; 1000 nodes x 32 heads: 262 and 295 us).
 // ------------------------------------------------------------------------------------------------
-__global__ void __launch_bounds__(kCombineThreads, 2) shared_combine_kernel(const SharedAttnParams p, int ncta) {
-  static_assert(4 * kCombineQuads * (kCombineThreads / 32) == 128, "a block covers the columns");
+template <int kJoinQuads, int kJoinBatch>
+__global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const SharedAttnParams p, int ncta) {
+  constexpr int kJoinParts = 128 / (4 * kJoinQuads * (kCombineThreads / 32));  // blocks to a row's columns
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention grid has completed
-  const int tid = threadIdx.x, lane = tid & 31, q0 = (tid >> 5) * kCombineQuads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (__syncthreads_or(tid < ncta && __ldcg(&p.cta_ok[tid]) == 0)) return;
   const long long rows = p.rows();
-  const int blocks = static_cast<int>((rows + 31) / 32);
-  for (long long item = blockIdx.x; item < static_cast<long long>(blocks) * p.hkv; item += gridDim.x) {
-    const int kvh = static_cast<int>(item / blocks);
-    const long long li = (item % blocks) * 32 + lane;
+  const long long blocks = (rows + 31) / 32;
+  for (long long item = blockIdx.x; item < blocks * p.hkv * kJoinParts; item += gridDim.x) {
+    const int q0 = (static_cast<int>(item % kJoinParts) * (kCombineThreads / 32) + warp) * kJoinQuads;
+    const int kvh = static_cast<int>(item / kJoinParts / blocks);
+    const long long li = (item / kJoinParts % blocks) * 32 + lane;
     if (li >= rows) continue;
+    const int4 at[2] = {__ldcg(p.row_at(0, kvh) + li), __ldcg(p.row_at(1, kvh) + li)};  // the second may be stale
     float M = -INFINITY, L = 0.f;
-    float4 acc[kCombineQuads];
+    float4 acc[kJoinQuads];
 #pragma unroll
-    for (int q = 0; q < kCombineQuads; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float2 ml, const float4 (&v)[kCombineQuads]) {
-      if (ml.x == -INFINITY) return;
-      const float top = fmaxf(M, ml.x);
-      const float a = ex2_approx(M - top), w = ex2_approx(ml.x - top);
-      L = fmaf(w, ml.y, L * a);
-#pragma unroll
-      for (int q = 0; q < kCombineQuads; ++q) {
-        acc[q].x = fmaf(w, v[q].x, acc[q].x * a);
-        acc[q].y = fmaf(w, v[q].y, acc[q].y * a);
-        acc[q].z = fmaf(w, v[q].z, acc[q].z * a);
-        acc[q].w = fmaf(w, v[q].w, acc[q].w * a);
-      }
-      M = top;
-    };
-    bool ok = true, shares = false;
+    for (int q = 0; q < kJoinQuads; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool ok = true;
+#pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
-      if (kind == 1 && !shares) break;
-      const int4 at = __ldcg(p.row_at(kind, kvh) + li);
-      if (kind == 0) shares = (at.x & kRowShares) != 0;
-      const int how = at.x & ~kRowShares;
-      float4 v[kCombineQuads];
-      if (how == kRowWhole) {
+      if (kind == 1 && !(at[0].x & kRowShares)) break;
+      const int how = at[kind].x & ~kRowShares;
+      ok = ok && (how == kRowWhole || how == kRowSplit);
+      if (!ok) break;
+      const int n = how == kRowSplit ? at[kind].z - at[kind].y + 1 : 1, qt = at[kind].w / kBM, r = at[kind].w % kBM;
+      for (int first = 0; first < n; first += kJoinBatch) {
+        float2 ml[kJoinBatch];
+        float4 v[kJoinBatch][kJoinQuads];
 #pragma unroll
-        for (int q = 0; q < kCombineQuads; ++q) v[q] = __ldcg(p.row_o(kind, kvh, q0 + q) + li);
-        add(__ldcg(p.row_ml(kind, kvh) + li), v);
-      } else if (how == kRowSplit) {
-        const int qt = at.w / kBM, r = at.w % kBM;
-        for (int c = at.y; c <= at.z; ++c) {
-          const int sl = slot_of(c, at.y) * kAttnQTiles + qt;
+        for (int j = 0; j < kJoinBatch; ++j) {
+          ml[j] = make_float2(-INFINITY, 0.f);
+          if (first + j >= n) continue;
+          if (how == kRowSplit) {
+            const int sl = slot_of(at[kind].y + first + j, at[kind].y) * kAttnQTiles + qt;
 #pragma unroll
-          for (int q = 0; q < kCombineQuads; ++q) v[q] = __ldcg(part_ptr(p, sl, q0 + q, r));
-          ok = ok && __ldcg(&p.part_ok[static_cast<long long>(sl) * kBM + r]) != 0;
-          add(__ldcg(&p.part_ml[static_cast<long long>(sl) * kBM + r]), v);
+            for (int q = 0; q < kJoinQuads; ++q) v[j][q] = __ldcg(part_ptr(p, sl, q0 + q, r));
+            ml[j] = __ldcg(&p.part_ml[static_cast<long long>(sl) * kBM + r]);
+            ok = ok && __ldcg(&p.part_ok[static_cast<long long>(sl) * kBM + r]) != 0;
+          } else {
+#pragma unroll
+            for (int q = 0; q < kJoinQuads; ++q) v[j][q] = __ldcg(p.row_o(kind, kvh, q0 + q) + li);
+            ml[j] = __ldcg(p.row_ml(kind, kvh) + li);
+          }
         }
-      } else {
-        ok = false;
+        float top = M;
+#pragma unroll
+        for (int j = 0; j < kJoinBatch; ++j) top = fmaxf(top, ml[j].x);
+        if (top == -INFINITY) continue;  // nothing visible so far
+        const float a = ex2_approx(M - top);  // 0 while M is still -inf
+        L *= a;
+#pragma unroll
+        for (int q = 0; q < kJoinQuads; ++q) {
+          acc[q].x *= a;
+          acc[q].y *= a;
+          acc[q].z *= a;
+          acc[q].w *= a;
+        }
+#pragma unroll
+        for (int j = 0; j < kJoinBatch; ++j) {
+          if (ml[j].x == -INFINITY) continue;
+          const float w = ex2_approx(ml[j].x - top);
+          L = fmaf(w, ml[j].y, L);
+#pragma unroll
+          for (int q = 0; q < kJoinQuads; ++q) {
+            acc[q].x = fmaf(w, v[j][q].x, acc[q].x);
+            acc[q].y = fmaf(w, v[j][q].y, acc[q].y);
+            acc[q].z = fmaf(w, v[j][q].z, acc[q].z);
+            acc[q].w = fmaf(w, v[j][q].w, acc[q].w);
+          }
+        }
+        M = top;
       }
     }
     if (!ok) continue;
@@ -1363,7 +1387,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2) shared_combine_kernel(cons
     const float inv = p.v_scale / L;  // the V cache's scale (1 for a bf16 cache)
     uint2* dst = reinterpret_cast<uint2*>(p.out + grow * 128 + q0 * 4);
 #pragma unroll
-    for (int q = 0; q < kCombineQuads; ++q)
+    for (int q = 0; q < kJoinQuads; ++q)
       dst[q] = make_uint2(pack_bf16x2(acc[q].x * inv, acc[q].y * inv), pack_bf16x2(acc[q].z * inv, acc[q].w * inv));
     if (q0 == 0 && p.lse != nullptr) p.lse[grow] = (M + __log2f(L)) * 0.69314718055994531f;
   }
@@ -1408,8 +1432,9 @@ cudaError_t launch_tree_attention_shared(const CUtensorMap& tm_q, const CUtensor
   const cudaError_t e = fp8_cache ? launch_attention<attn::Mode<true, true>>(tm_q, tm_k, tm_v, p, grid, stream)
                                   : launch_attention<attn::Mode<false, true>>(tm_q, tm_k, tm_v, p, grid, stream);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn::shared_combine_kernel, dim3(2 * grid), dim3(attn::kCombineThreads), 0, stream, nullptr, p,
-                    grid);
+  const bool few = p.rows() * p.hkv <= 32ll * 4 * grid;
+  return launch_pdl(few ? attn::shared_combine_kernel<1, 8> : attn::shared_combine_kernel<4, 2>, dim3(4 * grid),
+                    dim3(attn::kCombineThreads), 0, stream, nullptr, p, grid);
 }
 
 }  // namespace jf
