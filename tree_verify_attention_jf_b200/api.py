@@ -3,6 +3,7 @@ each function checks dtypes/shapes/devices, passes raw pointers to libjf.so (:mo
 Nothing here computes any part of the method."""
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
@@ -280,9 +281,29 @@ def _call(fn: str, dev: torch.device, stream, *args) -> None:
     if dev.type != "cuda":
         raise ValueError(f"the tensors must live on a CUDA device, got {dev}")
     s = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
-    with torch.cuda.device(dev):
-        code = getattr(_lib.lib(), fn)(*args, s)
+    call = getattr(_lib.lib(), fn)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        code = call(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            code = call(*args, s)
     _lib.check(fn, code)
+
+
+def _allocating_on(stream, dev: torch.device):
+    """Allocations for a call on a stream of the caller's come from that stream's memory: a block of another stream may
+    still be in use by work queued there."""
+    if stream is None or dev.type != "cuda":
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                             torch.cuda.ExternalStream(_stream(stream), device=dev))
+
+
+def _need_status(dev_status: Optional[torch.Tensor], dev: torch.device) -> None:
+    if dev_status is not None:
+        _need(dev_status, "dev_status", torch.int32, dev)
+        if dev_status.numel() < 1:
+            raise ValueError("dev_status must hold one int32")
 
 
 def _sampling_params(n: int, dev: torch.device, temperature, top_k, top_p, min_p) -> list:
@@ -297,11 +318,12 @@ def _sampling_params(n: int, dev: torch.device, temperature, top_k, top_p, min_p
     return [_ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p)]
 
 
-def _outputs(out: Optional[dict], dev: torch.device, **want) -> dict:
+def _outputs(out: Optional[dict], dev: torch.device, stream, **want) -> dict:
     """``out`` after a check of the tensors it holds, or newly allocated ones; want: name=(shape, dtype).  The last
     of the names, the log-probabilities, may be left out of ``out``."""
     if out is None:
-        return {k: torch.empty(shape, dtype=dtype, device=dev) for k, (shape, dtype) in want.items()}
+        with _allocating_on(stream, dev):
+            return {k: torch.empty(shape, dtype=dtype, device=dev) for k, (shape, dtype) in want.items()}
     for k, (shape, dtype) in want.items():
         if k == "logprob" and out.get(k) is None:
             continue
@@ -315,7 +337,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor, top
            top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None, out: Optional[dict] = None,
            dev_status: Optional[torch.Tensor] = None, stream=None) -> dict:
     """jf_sample: logits fp32 or bf16 [R, V] (rows may be strided, entries not), u and temperature fp32 [R] (u in
-    [0, 1); temperature 0 = greedy), top_k int32 [R] (0 = off), top_p fp32 [R] (1 = off), min_p fp32 [R] (0 = off), each
+    [0, 1); temperature 0 = greedy; the logits start on a 16-byte boundary), top_k int32 [R] (0 = off), top_p fp32 [R] (1 = off), min_p fp32 [R] (0 = off), each
     of the last three optional -> dict of token int32 [R] and logprob fp32 [R]."""
     dev = logits.device
     if logits.dtype not in _LOGITS_TYPE:
@@ -328,7 +350,8 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor, top
     if u.shape != (R,):
         raise ValueError(f"u must be [{R}], got {list(u.shape)}")
     params = _sampling_params(R, dev, temperature, top_k, top_p, min_p)
-    out = _outputs(out, dev, token=((R,), torch.int32), logprob=((R,), torch.float32))
+    _need_status(dev_status, dev)
+    out = _outputs(out, dev, stream, token=((R,), torch.int32), logprob=((R,), torch.float32))
     _call("jf_sample", dev, stream, _ptr(logits), _LOGITS_TYPE[logits.dtype], stride, R, V, _ptr(u), *params,
           _ptr(out["token"]), _ptr(out.get("logprob")), _ptr(dev_status))
     return out
@@ -357,7 +380,8 @@ def accept_sampled(token: torch.Tensor, parent: torch.Tensor, target_logits: tor
     if max_depth < 0 or u.shape != (B, max_depth + 1):
         raise ValueError(f"u must be [{B}, max_depth + 1] with max_depth >= 0, got {list(u.shape)}")
     params = _sampling_params(B, dev, temperature, top_k, top_p, min_p)
-    out = _outputs(out, dev, accepted_len=((B,), torch.int32), path=((B, max_depth + 1), torch.int32),
+    _need_status(dev_status, dev)
+    out = _outputs(out, dev, stream, accepted_len=((B,), torch.int32), path=((B, max_depth + 1), torch.int32),
                    bonus=((B,), torch.int32), logprob=((B, max_depth + 1), torch.float32))
     _call("jf_accept_sampled", dev, stream, _ptr(token), _ptr(parent), _ptr(target_logits),
           _LOGITS_TYPE[target_logits.dtype], _ptr(u), *params, B, N, V, max_depth, _ptr(out["accepted_len"]),
@@ -398,8 +422,10 @@ def _attention_shared(fn, cache_dtype, scales, q, k_cache, v_cache, block_table,
         raise ValueError("block_table must be [B, max_pages] and tree_offsets [B + 1]")
     if group_offsets.numel() != G + 1 or parent.numel() != T:
         raise ValueError("group_offsets must be [G + 1] for G shared_lens, parent [T]")
+    _need_status(dev_status, dev)
     if out is None:
-        out = torch.empty_like(q)
+        with _allocating_on(stream, dev):
+            out = torch.empty_like(q)
     _need(out, "out", torch.bfloat16, dev)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
@@ -408,9 +434,8 @@ def _attention_shared(fn, cache_dtype, scales, q, k_cache, v_cache, block_table,
         if lse.shape != (T, Hq):
             raise ValueError("lse must be [T, Hq]")
     if workspace is None:
-        workspace = SharedAttentionWorkspace(T, Hq, dev)
-        if stream is not None:  # the call runs on another stream than the one the scratch was allocated on
-            workspace.buf.record_stream(torch.cuda.ExternalStream(_stream(stream), device=dev))
+        with _allocating_on(stream, dev):  # freed on return, and not reused but on the same stream
+            workspace = SharedAttentionWorkspace(T, Hq, dev)
     _call(fn, dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), *scales, _ptr(block_table), block_table.shape[1],
           _ptr(prefix_lens), _ptr(tree_offsets), _ptr(parent), _ptr(group_offsets), _ptr(shared_lens), G, B, T, Hq, Hkv,
           D, page, num_pages, float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace.buf), workspace.nbytes,
