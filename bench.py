@@ -58,9 +58,9 @@ ATTN_SOURCES = ("tree_verify_attention_jf_b200/csrc/tree_attention.cu", "tree_ve
 # ncu capture of that workload), valid only for the kernel sources it was taken on: the roofline reports null once
 # any of them has changed.  Keys: bench workloads and legs.
 ATTN_TRAFFIC = {
-    "qwen3_30b_a3b": dict(bytes=331_310_080 + 21_271_040, source_sha256="c77f7b6b23b3b21b197d8eb90cb4a50a49a0de2978c769ccc8fa8f3d5d042b79"),
-    "qwen3_8b": dict(bytes=20_044_032 + 33_792, source_sha256="c77f7b6b23b3b21b197d8eb90cb4a50a49a0de2978c769ccc8fa8f3d5d042b79"),
-    "serving": dict(bytes=298_682_624 + 17_449_216, source_sha256="c77f7b6b23b3b21b197d8eb90cb4a50a49a0de2978c769ccc8fa8f3d5d042b79"),
+    "qwen3_30b_a3b": dict(bytes=330_625_024 + 20_950_272, source_sha256="ab96533196f3bf176fb23fda2347ab7c1c53f6f75d5a2e05f10402c5cd6803ac"),
+    "qwen3_8b": dict(bytes=20_043_776 + 34_560, source_sha256="ab96533196f3bf176fb23fda2347ab7c1c53f6f75d5a2e05f10402c5cd6803ac"),
+    "serving": dict(bytes=298_684_160 + 19_258_112, source_sha256="ab96533196f3bf176fb23fda2347ab7c1c53f6f75d5a2e05f10402c5cd6803ac"),
 }
 
 

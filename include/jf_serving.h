@@ -84,9 +84,10 @@ typedef enum {
  *   4. with W the weight kept, token[r] is the lowest kept id at which the running sum of the kept
  *      weights, taken in id order, exceeds u[r] * W; logprob[r] = ln(w_token / W).
  * T = 0 is greedy: the lowest id that attains m, logprob 0, whatever the other parameters are.
- * Weights are float64 and are summed as integers of 2^-f of the row's largest (f = min(48, 62 -
- * ceil(log2 vocab)), at least 43), so that every sum is exact and a result does not depend on the
- * order of the additions; a token lighter than 2^-(f+1) of the heaviest is never drawn.
+ * Weights are computed in float64 (relative error below 2^-45) and summed as integers of 2^-f of the
+ * row's largest (f = min(48, 62 - ceil(log2 vocab)), at least 43), so that every sum is exact and a
+ * result does not depend on the order of the additions, the size of the batch or the device's
+ * schedule; a token lighter than 2^-(f+1) of the heaviest is never drawn.
  * -inf logits (masked tokens) and NaN are no candidates.  A row without any candidate gives
  * token -1 and logprob -inf.  +inf logits share the weight equally among themselves.
  *

@@ -38,8 +38,9 @@ def shared_inputs(seed, hq, hkv, groups, nodes, suffixes, poison=True, scale=0.5
     to = np.concatenate([[0], np.cumsum(nodes)]).astype(np.int32)
     T = int(to[-1])
     draw = lambda *s: synth.bf16_round(rng.standard_normal(s, dtype=np.float32) * np.float32(scale))
-    inp = synth.AttentionInputs(q=draw(T, hq, 128), k_cache=draw(total, PAGE, hkv, 128), v_cache=draw(total, PAGE, hkv, 128),
-                                block_table=bt, prefix_lens=np.array(prefix, np.int32), tree_offsets=to,
+    inp = synth.AttentionInputs(q=draw(T, hq, 128), k_cache=draw(total, PAGE, hkv, 128),
+                                v_cache=draw(total, PAGE, hkv, 128), block_table=bt,
+                                prefix_lens=np.array(prefix, np.int32), tree_offsets=to,
                                 parent=np.concatenate(parents).astype(np.int32) if T else np.zeros(0, np.int32),
                                 sm_scale=128 ** -0.5, num_q_heads=hq, num_kv_heads=hkv)
     return inp, offs, shared

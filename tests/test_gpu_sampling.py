@@ -59,7 +59,7 @@ def run(x, u, par, dtype=torch.float32, pad=0, **kw):
 def check(x, u, par, got):
     tok, lp = got
     for r in range(x.shape[0]):
-        want, wlp = sample_row(x[r], float(u[r]), *(float(par[0][r]), int(par[1][r]), float(par[2][r]), float(par[3][r])))
+        want, wlp = sample_row(x[r], float(u[r]), float(par[0][r]), int(par[1][r]), float(par[2][r]), float(par[3][r]))
         assert tok[r] == want, (r, tok[r], want, [a[r] for a in par], u[r])
         if np.isinf(wlp):
             assert lp[r] == wlp
@@ -166,7 +166,8 @@ def test_bad_parameters_leave_their_row_unwritten():
     t[0], t[1], t[2], k[3], p[4], p[5], m[6], m[7], u[8], u[9], u[10] = (
         -1, np.nan, np.inf, -1, -0.1, 1.1, np.nan, 1.5, 1.0, -0.1, np.nan)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out = dict(token=torch.full((12,), -77, dtype=torch.int32, device="cuda"), logprob=torch.full((12,), 5.0, device="cuda"))
+    out = dict(token=torch.full((12,), -77, dtype=torch.int32, device="cuda"),
+               logprob=torch.full((12,), 5.0, device="cuda"))
     tok, lp = run(x, u, (t, k, p, m), out=out, dev_status=st)
     assert int(st.item()) == _lib.JF_ERR_DEVICE_CHECK
     assert (tok[:11] == -77).all() and (lp[:11] == 5.0).all()
@@ -336,5 +337,6 @@ def test_walk_refusals():
     with pytest.raises(ValueError):
         api.accept_sampled(tok, par, x[:, :, :7], u, t, 2)
     with pytest.raises(ValueError):
-        api.accept_sampled(tok, par, x, u, t, 2, out=dict(accepted_len=z(2, dt=torch.int32), path=z(2, 4, dt=torch.int32),
-                                                          bonus=z(2, dt=torch.int32)))
+        i = torch.int32
+        out = dict(accepted_len=z(2, dt=i), path=z(2, 4, dt=i), bonus=z(2, dt=i))
+        api.accept_sampled(tok, par, x, u, t, 2, out=out)

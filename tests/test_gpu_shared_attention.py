@@ -195,8 +195,9 @@ def test_device_checks():
 
 
 def test_workspace_is_reusable_and_graphs_replay():
-    cases = [shared_inputs(20 + i, 8, 2, g, n, s) for i, (g, n, s) in enumerate(
-        [([(3, 300)], [30, 2, 9], [5, 70, 0]), ([(1, 16), (2, 900)], [1, 1, 1], [1, 2, 3]), ([(2, 0)], [256, 5], [400, 0])])]
+    cases = [shared_inputs(20, 8, 2, [(3, 300)], [30, 2, 9], [5, 70, 0]),
+             shared_inputs(21, 8, 2, [(1, 16), (2, 900)], [1, 1, 1], [1, 2, 3]),
+             shared_inputs(22, 8, 2, [(2, 0)], [256, 5], [400, 0])]
     T = max(c[0].q.shape[0] for c in cases)
     ws = api.SharedAttentionWorkspace(T, 8, torch.device("cuda"))
     refs = [run(c, ws=ws) for c in cases]
@@ -245,8 +246,8 @@ def test_wait_that_runs_out_reports_timeout_and_writes_nothing():
     def call():
         code = L.jf_tree_attention_shared(
             *(d[k].data_ptr() for k in ("q", "k_cache", "v_cache", "block_table")), inp.block_table.shape[1],
-            *(t.data_ptr() for t in (d["prefix_lens"], d["tree_offsets"], d["parent"], g32, s32)), 1, 3, T, Hq, 1, 128, 16,
-            inp.k_cache.shape[0], inp.sm_scale, out.data_ptr(), None, ws.data_ptr(), ws.numel(), status.data_ptr(),
+            *(t.data_ptr() for t in (d["prefix_lens"], d["tree_offsets"], d["parent"], g32, s32)), 1, 3, T, Hq, 1, 128,
+            16, inp.k_cache.shape[0], inp.sm_scale, out.data_ptr(), None, ws.data_ptr(), ws.numel(), status.data_ptr(),
             torch.cuda.current_stream().cuda_stream)
         assert code == _lib.JF_OK
         torch.cuda.synchronize()

@@ -336,9 +336,9 @@ def _outputs(out: Optional[dict], dev: torch.device, stream, **want) -> dict:
 def sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor, top_k: Optional[torch.Tensor] = None,
            top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None, out: Optional[dict] = None,
            dev_status: Optional[torch.Tensor] = None, stream=None) -> dict:
-    """jf_sample: logits fp32 or bf16 [R, V] (rows may be strided, entries not), u and temperature fp32 [R] (u in
-    [0, 1); temperature 0 = greedy; the logits start on a 16-byte boundary), top_k int32 [R] (0 = off), top_p fp32 [R] (1 = off), min_p fp32 [R] (0 = off), each
-    of the last three optional -> dict of token int32 [R] and logprob fp32 [R]."""
+    """jf_sample: logits fp32 or bf16 [R, V] (rows may be strided, entries not; they start on a 16-byte boundary), u and
+    temperature fp32 [R] (u in [0, 1); temperature 0 = greedy), top_k int32 [R] (0 = off), top_p fp32 [R] (1 = off),
+    min_p fp32 [R] (0 = off), each of the last three optional -> dict of token int32 [R] and logprob fp32 [R]."""
     dev = logits.device
     if logits.dtype not in _LOGITS_TYPE:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
@@ -454,8 +454,8 @@ def tree_attention_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     in common; the whole pages of that prefix are read through the group's first block-table row, once for all its
     nodes.  Returns out."""
     return _attention_shared("jf_tree_attention_shared", torch.bfloat16, (), q, k_cache, v_cache, block_table,
-                             prefix_lens, tree_offsets, parent, group_offsets, shared_lens, sm_scale, out, lse, workspace,
-                             dev_status, stream)
+                             prefix_lens, tree_offsets, parent, group_offsets, shared_lens, sm_scale, out, lse,
+                             workspace, dev_status, stream)
 
 
 def tree_attention_shared_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float,

@@ -1,18 +1,22 @@
 // sampling.cuh -- drawing a token from one row of logits, by a thread-block cluster whose CTAs take a slice each.
 //
-// Mathematics.  With w_v = exp((x_v - m) / T) the filters min-p, top-k and top-p each keep a prefix of the candidates in
-// the order (x descending, id ascending), so the set kept is described by one cut (cut_x, cut_id): v is kept iff
+// Mathematics.  With w_v = exp((x_v - m) / T) the filters min-p, top-k and top-p each keep a prefix of the candidates
+// in the order (x descending, id ascending), so the set kept is described by one cut (cut_x, cut_id): v is kept iff
 // x_v > cut_x, or x_v == cut_x and v <= cut_id.  min-p is a cut at a value.  The top-k cut is the element of a given
-// rank, the top-p cut the element at which the running weight reaches a given mass.  Neither needs a sort of the row: a
-// histogram over m - x (any monotone function of x will do) names the bin that the border lies in.  When no more than
-// kList elements lie in that bin or above it, every CTA gets a list of them and finishes the draw by itself; otherwise
-// the bin's elements alone are listed to find the cut, and only if even those are too many (heavy ties) does cut_by_key()
-// narrow an interval of keys down to one value and its ids.  A small top-k needs no histogram of the row: the k-th
-// largest of a CTA's thread maxima bounds the CTA's k-th largest element from below, and few elements pass that bound.
+// rank, the top-p cut the element at which the running weight reaches a given mass.  Neither needs a sort of the row:
+// a histogram over m - x (any monotone function of x will do) names the bin that the border lies in.  When the elements
+// in that bin and above it fit a list, every CTA gets them and finishes the draw by itself; otherwise the bin's
+// elements alone are listed to find the cut, and only if even those are too many (heavy ties) does cut_by_key() narrow
+// an interval of keys down to one value and its ids.  A small top-k needs no histogram of the row: a few of a CTA's
+// thread maxima give a floor that few of its elements pass, and the list of all that do shows whether that was enough.
 // The draw is an inverse CDF over the kept weights in id order.
 //
 // Weights become 64-bit integers (multiples of 2^-f of the largest): integer sums are exact, so neither atomics nor the
 // split over CTAs changes a result.
+//
+// What bounds it: one pass over the weights takes 10 float64 instructions an element, of which an SM starts 64 a clock
+// (measured 4 elements a clock and SM); a barrier of the cluster takes 0.5 to 1 us, and a draw passes three (small
+// top-k) to eight of them.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -99,9 +103,9 @@ inline int sm_count() {
   return n;
 }
 
-// The widest cluster with which all rows (or sequences) run at once on an SM a CTA, while a slice keeps kMinSlice entries.
-// Clusters of 16 fill most of a GPC and wait for room once there are more than a few (8 walks of 11 steps: 318 us with 16
-// CTAs each, 267 us with 8; one walk of 6 steps: 58 and 65 us).
+// The widest cluster with which all rows (or sequences) run at once on an SM a CTA, while a slice keeps kMinSlice
+// entries.  Clusters of 16 fill most of a GPC and wait for room once there are more than a few (8 walks of 11 steps:
+// 318 us with 16 CTAs each, 267 us with 8; one walk of 6 steps: 58 and 65 us).
 inline int widest_cluster(long long rows, int vocab, int sms) {
   int c = 1;
   while (c < kMaxCluster && rows * 2 * c <= (c < 8 ? sms : sms / 2) && slice_len(vocab, c) > kMinSlice) c *= 2;
@@ -190,7 +194,8 @@ struct Drawn {
   bool mine;      // this thread writes the result (in one thread of the cluster)
 };
 
-// Descending bitonic sort of the first n2 entries (a power of two, 64 .. kList) of a list by all threads of the CTA.  Lane l of warp w holds entries 64 w + l and 64 w + 32 + l; steps over 32 or fewer entries are shuffles, a step over
+// Descending bitonic sort of the first n2 entries (a power of two, 64 .. kList) of a list by all threads of the CTA.
+// Lane l of warp w holds entries 64 w + l and 64 w + 32 + l; steps over 32 or fewer entries are shuffles, a step over
 // 64 or more goes through shared memory.
 __device__ __forceinline__ void sort_desc(u64* a, int n2) {
   const int tid = threadIdx.x, lane = tid & 31, i0 = 64 * (tid >> 5) + lane;
@@ -247,10 +252,10 @@ __device__ __forceinline__ void sort_desc(u64* a, int n2) {
   __syncthreads();
 }
 
-// One CTA's view of the row, whose slice its warps cut into ranges of consecutive ids.  kResident: the slice lies in shared
-// memory, brought there once by a bulk copy; otherwise every pass reads it from global memory (from L2 after the first).
-// Every member function is called by all threads of all CTAs of the cluster, in the same
-// order; the decisions between them follow from values that every CTA holds alike.
+// One CTA's view of the row, whose slice its warps cut into ranges of consecutive ids.  kResident: the slice lies in
+// shared memory, brought there once by a bulk copy; otherwise every pass reads it from global memory (from L2 after the
+// first).  Every member function is called by all threads of all CTAs of the cluster, in the same order; the decisions
+// between them follow from values that every CTA holds alike.
 template <typename T, bool kResident>
 struct Row {
   static_assert(kThreads >= kList / 2 && kThreads >= 8 * kSmall && kThreads >= kExpTab * kExpCopies, "work per thread");
@@ -289,9 +294,9 @@ struct Row {
   // The double 2^(52 - fx) + exp((x - m) / T), whose mantissa holds round(2^fx exp(..)), for x_zero <= x <= m.  With
   // (x - m) / T = (n + r) ln2 / 32, n integer and |r| <= 1/2, exp = 2^(n >> 5) 2^((n & 31) / 32) e^(r ln2 / 32), the
   // last factor by its Taylor series through the fifth power (truncation below 2^-48).  Exactly 2^fx at x = m.
-  // A table of 512 entries needs three terms only, but its lookups conflict (6 a clock and SM against 16 here).  There is
-  // no branch in it, so that a granule's exponentials run side by side: 11 float64 instructions each, of which an SM
-  // starts 64 a clock, are the bound of a pass over the weights.
+  // A table of 512 entries needs three terms only, but its lookups conflict (6 a clock and SM against 16 here).  There
+  // is no branch in it, so that a granule's exponentials run side by side (a branch for one special value cost a
+  // factor of three).
   __device__ __forceinline__ u64 weight_bits(float x) const {
     constexpr double kShift = 0x1.8p52;
     constexpr double a1 = 0.69314718055994530942 / kExpTab, a2 = a1 * a1 / 2, a3 = a2 * a1 / 3, a4 = a3 * a1 / 4,
@@ -315,8 +320,8 @@ struct Row {
     if (g > 0 && g < grans - 1) v = __ldcg(from + g);
     return v;
   }
-  // What load() gave, or the granule from s.edge: the first and the last of a slice in global memory may hold entries that
-  // are not the slice's, or not even the caller's.
+  // What load() gave, or the granule from s.edge: the first and the last of a slice in global memory may hold entries
+  // that are not the slice's, or not even the caller's.
   __device__ __forceinline__ void unpack(int g, uint4 v, float (&x)[kPer]) const {
     if (!kResident && (g == 0 || g == grans - 1)) v = s.edge[g == 0 ? 0 : 1];
     Granule<T>::unpack(v, x);
@@ -326,8 +331,8 @@ struct Row {
     g0 = min(grans, warp * gw);
     g1 = min(grans, g0 + gw);
   }
-  // f(g, x) for every granule of this warp's range, in the order of the ids over iterations and lanes; kBatch at a time, of
-  // which global memory's are all in flight together.
+  // f(g, x) for every granule of this warp's range, in the order of the ids over iterations and lanes; kBatch at a
+  // time, of which global memory's are all in flight together.
   template <int kBatch, typename F>
   __device__ __forceinline__ void walk(F f) const {
     int g0, g1;
@@ -458,7 +463,8 @@ struct Row {
     const uintptr_t a = (reinterpret_cast<uintptr_t>(row + lo) + 15) & ~uintptr_t(15);
     const uintptr_t e = reinterpret_cast<uintptr_t>(row + hi) & ~uintptr_t(15);
     if (a < e)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"(static_cast<uint32_t>(e - a)) : "memory");
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"(static_cast<uint32_t>(e - a))
+                   : "memory");
   }
 
   // Every CTA's pair of words, in s.xch[result] afterwards; a and b need to be valid in threads 0 .. C-1.
@@ -649,8 +655,8 @@ struct Row {
   __device__ __forceinline__ float below_bin(int bin) const {
     return bin_scale > 0.f && bin < kBins - 1 ? m - static_cast<float>(bin + 2) / bin_scale : -INFINITY;
   }
-  // Writes this CTA's kept elements from `floor` on to s.mine, with only >= 0 those of that bin alone; s.fill counts them,
-  // or exceeds kList.
+  // Writes this CTA's kept elements from `floor` on to s.mine, with only >= 0 those of that bin alone; s.fill counts
+  // them, or exceeds kList.
   __device__ __forceinline__ void gather(float floor, int only) {
     __syncthreads();
     if (tid == 0) s.fill = 0;
@@ -737,10 +743,10 @@ struct Row {
     return 0;
   }
 
-  // Lists a superset of the k largest kept elements in every CTA, in order: each CTA's elements from a floor on, which is
-  // the bin of the `local`-th largest of its thread maxima.  Elements missing lie below their CTA's floor, so the k
-  // largest are known if the k-th of the list reaches the highest floor; the number, or 0 if that does not work out (k too
-  // large, uneven CTAs, ties).
+  // Lists a superset of the k largest kept elements in every CTA, in order: each CTA's elements from a floor on, which
+  // is the bin of the `local`-th largest of its thread maxima.  Elements missing lie below their CTA's floor, so the k
+  // largest are known if the k-th of the list reaches the highest floor; the number, or 0 if that does not work out (k
+  // too large, uneven CTAs, ties).
   __device__ __forceinline__ int list_largest(int k) {
     const int room = kList / C, local = min(k, 3 * k / C + 8);
     if (local > room / 2 || local > kThreads / 2) return 0;
@@ -893,8 +899,8 @@ struct Row {
   }
 
   // Narrows the kept set to end at its element number `k` (mass false), or at the element where the running weight
-  // reaches `target` (mass true), whatever the values: an interval of keys is narrowed by histograms to one key.  The set
-  // is known to hold that much.
+  // reaches `target` (mass true), whatever the values: an interval of keys is narrowed by histograms to one key.  The
+  // set is known to hold that much.
   __device__ __forceinline__ void cut_by_key(bool mass, u64 target) {
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();  // no CTA reads the last histogram any more
@@ -964,8 +970,8 @@ struct Row {
   }
 
   // The lowest id at which the running sum of f, in id order, exceeds t, and its value; t is `fixed` if share < 0, else
-  // floor(share * total).  f(g, x, w) gives the terms of granule g, sum_of(g, x) their sum.  kAll: every thread of the cluster gets
-  // the result; otherwise the thread that returns true does, and all get the total.
+  // floor(share * total).  f(g, x, w) gives the terms of granule g, sum_of(g, x) their sum.  kAll: every thread of the
+  // cluster gets the result; otherwise the thread that returns true does, and all get the total.
   template <bool kAll, typename F, typename S>
   __device__ __forceinline__ bool find_id(u64 fixed, double share, F f, S sum_of, u64& total, int& id, float& at) {
     u64 sum = 0;
@@ -1056,8 +1062,8 @@ struct Row {
     return find_id<true>(t, -1.0, terms, sum_of, total, id, at);
   }
 
-  // The whole draw, after start() and with the row's parameters in s.rp.  kAll: the result is wanted in every thread; otherwise in
-  // the one whose result says so (and CTAs may return from here while others still work on their own).
+  // The whole draw, after start() and with the row's parameters in s.rp.  kAll: the result is wanted in every thread;
+  // otherwise in the one whose result says so (and CTAs may return from here while others still work on their own).
   template <bool kAll>
   __device__ __forceinline__ Drawn draw(uint32_t phase) {
     Drawn d{-1, -INFINITY, true, rank == 0 && tid == 0};
@@ -1080,7 +1086,7 @@ struct Row {
         if (rp.top_p < 1.0) n = max(1ull, static_cast<u64>(ceil(rp.top_p * static_cast<double>(n))));
         t = static_cast<u64>(static_cast<double>(u) * static_cast<double>(n));
       }
-      d.logprob = static_cast<float>(-log(static_cast<double>(n)));
+      d.logprob = n == 1 ? 0.f : static_cast<float>(-log(static_cast<double>(n)));
       return d;
     }
     c32 = rp.inv_t * (kExpTab / 0.69314718055994530942);

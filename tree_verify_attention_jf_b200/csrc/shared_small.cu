@@ -1,16 +1,17 @@
 // shared_small.cu -- the own keys of sequences with few query rows, for tree attention over a shared prefix (sm_100a).
 //
-// What it computes: the softmax state (unnormalised O, running max, row sum) of a sequence's rows against the slots that
-// it does not share, for sequences whose N tree nodes x g query heads make at most 16 rows and whose own slots are few
-// (small_sequence()).  The persistent kernel of tree_attention.cu gives every (sequence, kv head) a pair of 128-row M
-// tiles and a pipeline to fill, which for one decoded token and a hundred keys costs about ten times the keys' bytes: 64
-// single tokens with 16384 shared and up to 256 own slots took 102 us, of which the shared part is about 30.
+// What it computes: the softmax state (unnormalised O, running max, row sum) of a sequence's rows against the slots
+// that it does not share, for sequences whose N tree nodes x g query heads make at most 16 rows and whose own slots are
+// few (small_sequence()).  The persistent kernel of tree_attention.cu gives every (sequence, kv head) a pair of 128-row
+// M tiles and a pipeline to fill, which for one decoded token and a hundred keys costs far more than the keys' bytes:
+// 64 single tokens with 16384 shared and up to 256 own slots (8 kv heads) took 102 us a call without this kernel and
+// 75 with it.
 //
 // Design: bound by latency, then by the cache's bytes.  One CTA of four warps per (sequence, kv head); a warp takes a
 // page (16 keys) at a time and multiplies it with mma.sync, whose 16 rows fit the few query rows where a tcgen05 tile
-// would be almost empty.  Both products are invariant to a permutation of the contracted index, and the outputs to one of
-// the columns, so operands are permuted to let every thread load consecutive bytes straight from the cache: thread t of a
-// quad holds elements 32 t .. 32 t + 31 of its key's row, and 16 consecutive dims of its four V rows.
+// would be almost empty.  Both products are invariant to a permutation of the contracted index, and the outputs to one
+// of the columns, so operands are permuted to let every thread load consecutive bytes straight from the cache: thread t
+// of a quad holds elements 32 t .. 32 t + 31 of its key's row, and 16 consecutive dims of its four V rows.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -78,8 +79,8 @@ __device__ __forceinline__ void load_row(const void* cache, long long element, u
 
 template <bool kFp8>
 __global__ void __launch_bounds__(kThreads)
-    small_kernel(const __nv_bfloat16* __restrict__ q, const void* __restrict__ k_cache, const void* __restrict__ v_cache,
-                 const SharedAttnParams p) {
+    small_kernel(const __nv_bfloat16* __restrict__ q, const void* __restrict__ k_cache,
+                 const void* __restrict__ v_cache, const SharedAttnParams p) {
   __shared__ float s_o[kWarps][kRows][kHeadDim + 4];
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ int s_parent[kRows];
@@ -88,8 +89,8 @@ __global__ void __launch_bounds__(kThreads)
   const int kvh = blockIdx.x, b = blockIdx.y;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before this one (which may produce any input)
-  // the sequence; malformed offsets or lengths are left to the other kernel, which reports them.  (The loads that do not
-  // depend on the group go first.)
+  // the sequence; malformed offsets or lengths are left to the other kernel, which reports them.  (The loads that do
+  // not depend on the group go first.)
   const int off = __ldg(p.tree_offsets + b), N = __ldg(p.tree_offsets + b + 1) - off, P = __ldg(p.prefix_lens + b);
   int lo = 0, hi = p.num_groups - 1;  // the last group that starts at or before b
   while (lo < hi) {

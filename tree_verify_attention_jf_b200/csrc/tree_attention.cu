@@ -296,7 +296,8 @@ __device__ void build_shared_plan(Smem& s, const SharedAttnParams& p) {
     if (P < 0 || N < 0 || N > kMaxTreeNodes || p.group_offsets[lo] > b || p.group_offsets[lo + 1] <= b) bad = 1;
     // what is shared is part of the sequence's prefix, and its table has room for the slots; the item of one that
     // says otherwise is walked over its first pages and not stored
-    const bool fits = P >= p.shared_lens[lo] && static_cast<long long>(P) + N <= static_cast<long long>(p.max_pages) * kPage;
+    const bool fits = P >= p.shared_lens[lo] &&
+                      static_cast<long long>(P) + N <= static_cast<long long>(p.max_pages) * kPage;
     s.item_x[G + b] = fits ? shared : -1;
     s.seq_p[G + b] = fits ? P - shared * kPage : 0;
     s.seq_off[G + b] = off;
@@ -1302,10 +1303,10 @@ __global__ void __launch_bounds__(kCombineThreads, 2) combine_kernel(const AttnP
 
 // ------------------------------------------------------------------------------------------------
 // Shared prefix: joins every row's two states, each whole or in the parts of a split unit, and stores the output.  A
-// warp takes 32 rows of one kv head (one per lane) and 4 * kJoinQuads columns; a row's parts (the prefix of a few rows is
-// cut over up to all CTAs) are loaded kJoinBatch at a time.  Few rows are spread over four times the warps by narrow
-// columns, where many would read their descriptors four times for nothing (64 single tokens: 79 -> 74 us a call with
-// narrow columns; 1000 nodes x 32 heads: 262 and 295 us).
+// warp takes 32 rows of one kv head (one per lane) and 4 * kJoinQuads columns; a row's parts (the prefix of a few rows
+// is cut over up to all CTAs) are loaded kJoinBatch at a time.  Few rows are spread over four times the warps by narrow
+// columns, where many would read their descriptors four times for nothing (64 single tokens with 32 heads: 79 us a call
+// with wide columns, 74 with narrow ones; 1000 nodes: 262 and 295 us).
 // ------------------------------------------------------------------------------------------------
 template <int kJoinQuads, int kJoinBatch>
 __global__ void __launch_bounds__(kCombineThreads) shared_combine_kernel(const SharedAttnParams p, int ncta) {
