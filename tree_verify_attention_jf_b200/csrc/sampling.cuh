@@ -651,30 +651,36 @@ struct Row {
     return s.bin < kBins;
   }
 
-  // A value below every value of the bin, by less than two bins.
+  // A value below every value of the bin, and one above every value, each by less than two bins.
   __device__ __forceinline__ float below_bin(int bin) const {
     return bin_scale > 0.f && bin < kBins - 1 ? m - static_cast<float>(bin + 2) / bin_scale : -INFINITY;
   }
+  __device__ __forceinline__ float above_bin(int bin) const {
+    return bin_scale > 0.f && bin > 2 ? m - static_cast<float>(bin - 2) / bin_scale : INFINITY;
+  }
   // Writes this CTA's kept elements from `floor` on to s.mine, with only >= 0 those of that bin alone; s.fill counts
-  // them, or exceeds kList.
+  // them, or exceeds kList.  Few are: most granules end at the comparison with the two bounds.
   __device__ __forceinline__ void gather(float floor, int only) {
     __syncthreads();
     if (tid == 0) s.fill = 0;
     __syncthreads();
-    walk<2>([&](int g, const float(&x)[kPer]) {
-      float top_x = fmax3(x[0], x[1], x[2]);
+    const float ceiling = only >= 0 ? above_bin(only) : INFINITY;
+    walk<4>([&](int g, const float(&x)[kPer]) {
+      uint32_t hits = 0;
 #pragma unroll
-      for (int e = 3; e < kPer; ++e) top_x = fmaxf(top_x, x[e]);
-      if (!(top_x >= floor) || *static_cast<volatile uint32_t*>(&s.fill) > kList) return;
+      for (int e = 0; e < kPer; ++e) hits |= x[e] >= floor && x[e] <= ceiling ? 1u << e : 0u;
+      if (hits == 0 || *static_cast<volatile uint32_t*>(&s.fill) > kList) return;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        if (!(x[e] >= floor) || !kept(x[e], id_of(g, e)) || (only >= 0 && bin_of(x[e]) != only)) continue;
-        const cg::coalesced_group hits = cg::coalesced_threads();  // one addition for all lanes that are here
-        uint32_t at = 0;
-        if (hits.thread_rank() == 0) at = atomicAdd(&s.fill, hits.size());
-        at = hits.shfl(at, 0) + hits.thread_rank();
-        if (at < kList) s.mine[at] = static_cast<u64>(ord32(x[e])) << 32 | static_cast<uint32_t>(~id_of(g, e));
-      }
+      for (int e = 0; e < kPer; ++e)
+        if (!kept(x[e], id_of(g, e)) || (only >= 0 && bin_of(x[e]) != only)) hits &= ~(1u << e);
+      if (hits == 0) return;
+      uint32_t at = atomicAdd(&s.fill, static_cast<uint32_t>(__popc(hits)));
+#pragma unroll
+      for (int e = 0; e < kPer; ++e)
+        if (hits >> e & 1) {
+          if (at < kList) s.mine[at] = static_cast<u64>(ord32(x[e])) << 32 | static_cast<uint32_t>(~id_of(g, e));
+          ++at;
+        }
     });
     __syncthreads();
   }
