@@ -332,7 +332,8 @@ struct Row {
     g1 = min(grans, g0 + gw);
   }
   // f(g, x) for every granule of this warp's range, in the order of the ids over iterations and lanes; kBatch at a
-  // time, of which global memory's are all in flight together.
+  // time, and those from global memory are loaded while the batch before them is worked on (256 rows of 151936 float32
+  // entries, loaded right before their use: no filter 114 us instead of 105, top-p 295 instead of 278).
   template <int kBatch, typename F>
   __device__ __forceinline__ void walk(F f) const {
     int g0, g1;
@@ -346,12 +347,18 @@ struct Row {
       }
       return;
     }
+    uint4 nx[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (g0 + lane + i * 32 < g1) nx[i] = load(g0 + lane + i * 32);
 #pragma unroll 1
     for (int g = g0 + lane; g < g1; g += kBatch * 32) {
       uint4 v[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (g + i * 32 < g1) v[i] = load(g + i * 32);
+      for (int i = 0; i < kBatch; ++i) {
+        v[i] = nx[i];
+        if (g + (i + kBatch) * 32 < g1) nx[i] = load(g + (i + kBatch) * 32);
+      }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
         if (g + i * 32 < g1) {
@@ -587,7 +594,7 @@ struct Row {
   __device__ __forceinline__ bool find_bin(bool mass, u64 k, double share) {
     clear_bins();
     if (mass) {
-      walk<2>([&](int g, const float(&x)[kPer]) {
+      walk<1>([&](int g, const float(&x)[kPer]) {
         u64 w[kPer];
         if (weights(g, x, w)) add_masses(x, w);
       });
@@ -665,7 +672,7 @@ struct Row {
     if (tid == 0) s.fill = 0;
     __syncthreads();
     const float ceiling = only >= 0 ? above_bin(only) : INFINITY;
-    walk<4>([&](int g, const float(&x)[kPer]) {
+    walk<2>([&](int g, const float(&x)[kPer]) {
       uint32_t hits = 0;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) hits |= x[e] >= floor && x[e] <= ceiling ? 1u << e : 0u;
@@ -981,7 +988,7 @@ struct Row {
   template <bool kAll, typename F, typename S>
   __device__ __forceinline__ bool find_id(u64 fixed, double share, F f, S sum_of, u64& total, int& id, float& at) {
     u64 sum = 0;
-    walk<2>([&](int g, const float(&x)[kPer]) { sum += sum_of(g, x); });
+    walk<1>([&](int g, const float(&x)[kPer]) { sum += sum_of(g, x); });
     sum = warp_sum_u64(sum);
     __syncthreads();
     if (lane == 0) s.wsum[0][warp] = sum;
