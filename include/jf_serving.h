@@ -88,6 +88,8 @@ typedef enum {
  * row's largest (f = min(48, 62 - ceil(log2 vocab)), at least 43), so that every sum is exact and a
  * result does not depend on the order of the additions, the size of the batch or the device's
  * schedule; a token lighter than 2^-(f+1) of the heaviest is never drawn.
+ * logprob is off by at most vocab * 2^-(f+1) (2^-25 for the largest vocabulary), beside its own
+ * rounding to float32.
  * -inf logits (masked tokens) and NaN are no candidates.  A row without any candidate gives
  * token -1 and logprob -inf.  +inf logits share the weight equally among themselves.
  *

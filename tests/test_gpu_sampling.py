@@ -340,3 +340,37 @@ def test_walk_refusals():
         i = torch.int32
         out = dict(accepted_len=z(2, dt=i), path=z(2, 4, dt=i), bonus=z(2, dt=i))
         api.accept_sampled(tok, par, x, u, t, 2, out=out)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["none", "top_p", "all"])
+def test_rows_behind_two_to_the_31_entries(dtype, kind):
+    R, V, stride = 3, 5000, 2 ** 30 + 3
+    x, rng = make_rows(41, R, V)
+    if dtype == torch.bfloat16:
+        x = bf16(x)
+    par, u = params(rng, R, kind), rng.random(R, dtype=np.float32)
+    rows = torch.empty(2 * stride + V, dtype=dtype, device="cuda").as_strided((R, V), (stride, 1))
+    rows.copy_(dev(x, dtype))
+    got = api.sample(rows, dev(u), *(dev(a) for a in par))
+    check(x, u, par, (got["token"].cpu().numpy(), got["logprob"].cpu().numpy()))
+
+
+def test_walk_behind_two_to_the_31_entries():
+    B, N, V, D = 5, 1024, 524288, 2
+    rng = np.random.default_rng(42)
+    x, u = bf16(make_rows(43, 1, V)[0]), rng.random((B, D + 1), dtype=np.float32)
+    par = [np.ones(B, np.float32), np.full(B, 50, np.int32)]
+    logits = torch.zeros(B, N, V, dtype=torch.bfloat16, device="cuda")
+    logits[B - 1] = dev(x, torch.bfloat16)
+    token, parent = np.zeros((B, N), np.int32), np.zeros((B, N), np.int32)
+    want = [sample_row(x[0], float(u[B - 1, i]), 1.0, 50, 1.0, 0.0) for i in range(D + 1)]
+    parent[:, 0] = -1
+    parent[:, N - 1] = N - 2  # root, node N - 2, node N - 1
+    token[B - 1, N - 2:] = [want[0][0], want[1][0]]
+    token[B - 1, 1:N - 2] = -1
+    got = api.accept_sampled(dev(token), dev(parent), logits, dev(u), dev(par[0]), D, top_k=dev(par[1]))
+    assert int(got["accepted_len"][B - 1]) == D and got["path"][B - 1].tolist()[1:] == [N - 2, N - 1]
+    assert int(got["bonus"][B - 1]) == want[D][0]
+    lp = got["logprob"][B - 1].cpu().numpy()
+    assert all(abs(lp[i] - want[i][1]) <= LP_REL * abs(want[i][1]) + LP_ABS for i in range(D + 1))

@@ -290,3 +290,36 @@ def test_refusals():
         call(workspace=api.SharedAttentionWorkspace(1, 1, torch.device("cuda")))
     with pytest.raises(_lib.JFError):
         call(group_offsets=i32([0, 1, 2, 2]), shared_lens=i32([0, 0, 0]))  # more groups than sequences
+
+
+def test_workspace_of_another_device_is_refused():
+    inp, go, sl = shared_inputs(33, 4, 1, [(2, 32)], [3, 2], [0, 4])
+    ws = api.SharedAttentionWorkspace(5, 4, torch.device("cpu"))
+    with pytest.raises(ValueError, match="workspace"):
+        run((inp, go, sl), ws=ws)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("nodes", [[1, 1, 2], [40, 1, 30]])
+def test_pages_behind_two_to_the_31_entries(fp8, nodes):
+    hkv = 8
+    inp, go, sl = shared_inputs(34, 2 * hkv, hkv, [(2, 144), (1, 0)], nodes, [5, 40, 33])
+    first = 2 ** 31 // (16 * hkv * 128)  # the pages move up by 2^31 entries
+    d = to_dev(inp)
+    d["block_table"] = torch.where(d["block_table"] >= 0, d["block_table"] + first, d["block_table"])
+    pages, st = inp.k_cache.shape[0], torch.zeros(1, dtype=torch.int32, device="cuda")
+    caches = []
+    for c, s in zip((inp.k_cache, inp.v_cache), SCALES):
+        c = torch.from_numpy(synth.e4m3_cache(c, s)).cuda() if fp8 else torch.from_numpy(c).cuda().bfloat16()
+        big = torch.zeros((first + pages, *c.shape[1:]), dtype=c.dtype, device="cuda")
+        big[first:] = c
+        caches.append(big)
+    rest = (d["block_table"], d["prefix_lens"], d["tree_offsets"], d["parent"], i32(go), i32(sl), inp.sm_scale)
+    lse = torch.full(inp.q.shape[:2], float("nan"), device="cuda")
+    if fp8:
+        out = api.tree_attention_shared_fp8(d["q"], *caches, *SCALES, *rest, lse=lse, dev_status=st)
+    else:
+        out = api.tree_attention_shared(d["q"], *caches, *rest, lse=lse, dev_status=st)
+    assert int(st.item()) == 0
+    ref, lref = oracle((inp, go, sl), fp8)
+    compare(out.float().cpu().numpy(), ref, lse.cpu().numpy(), lref)

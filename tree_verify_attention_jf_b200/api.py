@@ -436,6 +436,8 @@ def _attention_shared(fn, cache_dtype, scales, q, k_cache, v_cache, block_table,
     if workspace is None:
         with _allocating_on(stream, dev):  # freed on return, and not reused but on the same stream
             workspace = SharedAttentionWorkspace(T, Hq, dev)
+    elif workspace.buf.device != dev:
+        raise ValueError(f"the workspace must be on {dev}, got {workspace.buf.device}")
     _call(fn, dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), *scales, _ptr(block_table), block_table.shape[1],
           _ptr(prefix_lens), _ptr(tree_offsets), _ptr(parent), _ptr(group_offsets), _ptr(shared_lens), G, B, T, Hq, Hkv,
           D, page, num_pages, float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace.buf), workspace.nbytes,

@@ -3,8 +3,9 @@
 // Design: a thread-block cluster takes a row.  While few rows are asked for, its CTAs hold the row in shared memory, so
 // that each pass of the draw (sampling.cuh) is short; with many rows the barriers of wide clusters would dominate, and
 // narrow clusters, down to one CTA a row, read the row again from L2 in each pass.  Measured on rows of 151936 float32
-// entries with top-p alone (us; held in shared memory / read from memory, each by its best number of CTAs): 8 rows 40
-// (8) / 48 (8); 32 rows 56 (4) / 73 (4); 64 rows 106 (4) / 99 (4); 128 rows 188 (4) / 166 (2); 256 rows 358 (4) / 315 (1).
+// entries with top-p alone (us; held in shared memory / read from memory, with the number of CTAs): 8 rows 31 (8) / 37
+// (16); 32 rows 46 (4) / 55 (8); 64 rows 123 (8) / 87 (4); 128 rows 227 (8) / 147 (2); 256 rows - / 273 (2), 278 (1).
+// Without filters, read from memory: 256 rows 108 (2) / 105 (1); 512 rows 183 (2) / 201 (1).
 #include "sampling.cuh"
 
 namespace jf {
