@@ -149,6 +149,35 @@ def test_temperatures_from_tiny_to_huge():
         check(x, u, par, run(x, u, par))
 
 
+# (m, T) where one float32 step below m is about 954, 977, 1024 and 60 times T
+STEPS = [(10.0, 1e-9), (1e4, 1e-6), (1e10, 1.0), (-3e38, 3.4e29), (2.0, 2e-9)]
+
+
+def step_rows(rng, V, dtype):
+    """A row per entry of STEPS: the maximum at two places and its neighbours, one to four steps below, at many."""
+    x = np.empty((len(STEPS), V), np.float32)
+    for r, (m, _) in enumerate(STEPS):
+        v = [torch.tensor(m, dtype=dtype)]
+        for _ in range(4):
+            v.append(torch.nextafter(v[-1], torch.tensor(-np.inf, dtype=dtype)))
+        v = torch.stack(v).float().numpy()
+        x[r] = v[rng.integers(1, 5, V)]
+        x[r, rng.choice(V, 2, replace=False)] = v[0]
+    return x
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [40, 4099, 120001])
+def test_logits_one_step_below_the_largest_at_tiny_temperatures(dtype, V):
+    rng = np.random.default_rng(V)
+    x, R = step_rows(rng, V, dtype), len(STEPS)
+    t = np.array([T for _, T in STEPS], np.float32)
+    for k, p, m in ((0, 1, 0), (0, 0.9, 0), (20, 1, 0), (V // 2, 1, 0), (V // 2, 0.8, 0), (0, 1, 0.3)):
+        par = (t, np.full(R, k, np.int32), np.full(R, p, np.float32), np.full(R, m, np.float32))
+        u = rng.uniform(0.02, 0.98, R).astype(np.float32)  # u = 0 may draw what weighs less than the sums resolve
+        check(x, u, par, run(x, u, par, dtype, pad=3))
+
+
 def test_parameters_left_out_are_off():
     x, rng = make_rows(5, 4, 700)
     t, u = rng.uniform(0.5, 1, 4).astype(np.float32), rng.random(4, dtype=np.float32)
@@ -278,6 +307,21 @@ def test_walk_stops_at_a_row_without_candidates():
     got = api.accept_sampled(dev(token), dev(parent), dev(x), dev(u), dev(par[0]), 8)
     check_walk((token, parent, x, u), par, 8, got)
     assert int(got["bonus"][1]) == -1 and int(got["accepted_len"][1]) == 0
+
+
+@pytest.mark.parametrize("kind", ["none", "top_p", "top_k"])
+def test_walk_over_logits_one_step_below_the_largest(kind):
+    rng = np.random.default_rng(10)
+    B, N, V, D = len(STEPS), 12, 2003, 6
+    x = np.stack([step_rows(rng, V, torch.float32) for _ in range(N)], 1)
+    par = list(params(rng, B, kind))
+    par[0] = np.array([T for _, T in STEPS], np.float32)
+    parent = np.tile(np.arange(-1, N - 1, dtype=np.int32), (B, 1))  # a chain that carries one of the two maxima
+    token = np.zeros((B, N), np.int32)
+    token[:, 1:] = x[:, :-1].argmax(-1)
+    u = rng.uniform(0.02, 0.98, (B, D + 1)).astype(np.float32)
+    got = api.accept_sampled(dev(token), dev(parent), dev(x), dev(u), dev(par[0]), D, *(dev(a) for a in par[1:]))
+    assert check_walk((token, parent, x, u), par, D, got).max() > 0
 
 
 def test_walk_device_checks_leave_the_sequence_unwritten():

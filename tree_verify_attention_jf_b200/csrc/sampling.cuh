@@ -1121,7 +1121,9 @@ struct Row {
       return d;
     }
     c32 = rp.inv_t * (kExpTab / 0.69314718055994530942);
-    x_zero = __double2float_rd(md - (fx + 2) * 0.69314718055994530942 * rp.t);
+    // Rounded up: a float32 logit is at or above it exactly when it is at or above the bound itself.  Rounded down, the
+    // step below a large m could lie hundreds of T under it, where weight_bits() has no exponent left.
+    x_zero = __double2float_ru(md - (fx + 2) * 0.69314718055994530942 * rp.t);
     set_cut(fmaxf(__double2float_ru(md + rp.ln_min_p_t), -3.402823466e38f), INT_MAX);
     set_bins(rp);
     // top-k by the count, then top-p by the weight; a list that holds all that is kept ends the draw
