@@ -194,6 +194,36 @@ def test_device_checks():
     expect((dataclasses.replace(inp, prefix_lens=pl), go, sl), [1])
 
 
+def test_malformed_lengths_of_one_sequence_leave_the_batch_unwritten():
+    # found by the plan's second check, each by one thread of few: all others must agree to leave
+    rng = np.random.default_rng(14)
+    B = 600
+    nodes = rng.integers(0, 4, B)
+    nodes[[0, 299, 300, B - 1]] = [2, 200, 200, 2]
+    inp, go, sl = shared_inputs(14, 4, 1, [(300, 48), (299, 16), (1, 0)], nodes, rng.integers(0, 40, B))
+    ws = api.SharedAttentionWorkspace(inp.q.shape[0], 4, torch.device("cuda"))
+    ref, lref = run((inp, go, sl), ws=ws)
+    lengths = []
+    for b in (0, 299, 301, B - 1):
+        pl = inp.prefix_lens.copy()
+        pl[b] = -1
+        lengths.append(dict(prefix_lens=pl))
+    for b, to in ((300, inp.tree_offsets[299]), (300, inp.tree_offsets[301])):
+        off = inp.tree_offsets.copy()
+        off[b] = to                       # 400 nodes in one tree, none in the other
+        lengths.append(dict(tree_offsets=off))
+    off = inp.tree_offsets.copy()
+    off[1] = off[2] + 1                   # decreasing
+    lengths.append(dict(tree_offsets=off))
+    for bad in lengths:
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = run((dataclasses.replace(inp, **bad), go, sl), ws=ws, status=st)
+        assert int(st.item()) == _lib.JF_ERR_DEVICE_CHECK
+        assert np.isnan(out).all() and np.isnan(lse).all()
+    out, lse = run((inp, go, sl), ws=ws)
+    assert np.array_equal(out, ref) and np.array_equal(lse, lref)
+
+
 def test_workspace_is_reusable_and_graphs_replay():
     cases = [shared_inputs(20, 8, 2, [(3, 300)], [30, 2, 9], [5, 70, 0]),
              shared_inputs(21, 8, 2, [(1, 16), (2, 900)], [1, 1, 1], [1, 2, 3]),

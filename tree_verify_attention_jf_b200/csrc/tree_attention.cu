@@ -262,8 +262,15 @@ __device__ void build_shared_plan(Smem& s, const SharedAttnParams& p) {
   const int tid = threadIdx.x;
   const int B = p.batch, G = p.num_groups, I = G + B;
   if (tid == 0) s.bad_meta = 0;
-  __syncthreads();
   int bad = 0;
+  // Each of the two checks is decided by the barrier itself: all threads leave or none does, however far apart the
+  // warps run.
+  auto reject = [&]() {
+    if (!__syncthreads_or(bad)) return false;
+    if (tid == 0) s.bad_meta = 1;
+    __syncthreads();
+    return true;
+  };
   if (tid == 0 && (p.tree_offsets[0] != 0 || p.tree_offsets[B] != p.total_nodes || p.group_offsets[0] != 0 ||
                    p.group_offsets[G] != B))
     bad = 1;
@@ -282,9 +289,7 @@ __device__ void build_shared_plan(Smem& s, const SharedAttnParams& p) {
     s.seq_p[g] = fits ? shared * kPage : kPage;
     s.seq_off[g] = o0;
   }
-  if (bad) atomicOr(&s.bad_meta, 1);
-  __syncthreads();
-  if (s.bad_meta) return;
+  if (reject()) return;
   for (int b = tid; b < B; b += kThreads) {
     int lo = 0, hi = G - 1;  // the last group that starts at or before b
     while (lo < hi) {
@@ -304,9 +309,7 @@ __device__ void build_shared_plan(Smem& s, const SharedAttnParams& p) {
     // a small sequence's own keys are another kernel's work
     s.item_n[G + b] = p.small && fits && N > 0 && small_sequence(N, p.group, P - shared * kPage + N) ? 0 : N;
   }
-  if (bad) atomicOr(&s.bad_meta, 1);
-  __syncthreads();
-  if (s.bad_meta) return;
+  if (reject()) return;
   const int per = (I + kThreads - 1) / kThreads;
   const int i0 = tid * per;
   auto cost = [&](int i) {
