@@ -83,6 +83,15 @@ def test_attention_shared_host_validation(L, fp8):
     assert size(10, 4) < size(11, 4) < size(11, 32) and size(10, 4) % 256 == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_attention_shared_refuses_counts_whose_sum_passes_32_bits(L, fp8):
+    # no nodes: nothing is launched even where the call is taken
+    fn = L.jf_tree_attention_shared_fp8 if fp8 else L.jf_tree_attention_shared
+    for B, G in ((2 ** 31 - 1, 1), (2 ** 30, 2 ** 30), (2 ** 31 - 1, 2 ** 31 - 1)):
+        assert fn(16, 32, 48, *((0.1, 0.1) if fp8 else ()), 64, 4, 64, 64, 64, 64, 64, G, B, 0, 4, 1, 128, 16, 8, 0.1,
+                  64, None, 256, 1 << 40, None, None) == UNSUP
+
+
 def test_python_calls_refuse_cpu_tensors():
     x, u, t = torch.zeros(2, 8), torch.zeros(2), torch.ones(2)
     with pytest.raises(ValueError, match="CUDA"):
