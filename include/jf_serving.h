@@ -33,7 +33,8 @@ extern "C" {
  *
  * Layouts: as jf_tree_attention, and group_offsets int32 [num_groups+1], group_offsets[0] = 0,
  *          non-decreasing, group_offsets[num_groups] = batch; shared_lens int32 [num_groups], >= 0.
- * Limits: as jf_tree_attention, and batch + num_groups <= 1024, 1 <= num_groups <= batch.
+ * Limits: as jf_tree_attention, and batch + num_groups <= 1024, 1 <= num_groups <= batch,
+ *          max_pages_per_seq <= 2^27 - 16.
  * Device checks (JF_ERR_DEVICE_CHECK): those of jf_tree_attention; a sequence whose prefix is
  *          shorter than its group's shared_lens is left unwritten; a page id out of range among the
  *          shared ones, or more of them than the block table holds, leaves the whole group unwritten;

@@ -92,6 +92,15 @@ def test_attention_shared_refuses_counts_whose_sum_passes_32_bits(L, fp8):
                   64, None, 256, 1 << 40, None, None) == UNSUP
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_attention_shared_refuses_tables_of_more_slots_than_32_bits_count(L, fp8):
+    # a prefix of almost 2^31 slots fits such a table, and its tiles would be counted in 32 bits; no nodes, as above
+    fn = L.jf_tree_attention_shared_fp8 if fp8 else L.jf_tree_attention_shared
+    for pages, want in (((1 << 27) - 16, OK), ((1 << 27) - 15, UNSUP), (1 << 27, UNSUP), (2 ** 31 - 1, UNSUP)):
+        assert fn(16, 32, 48, *((0.1, 0.1) if fp8 else ()), 64, pages, 64, 64, 64, 64, 64, 1, 3, 0, 4, 1, 128, 16, 8, 0.1,
+                  64, None, 256, 1 << 40, None, None) == want, pages
+
+
 def test_python_calls_refuse_cpu_tensors():
     x, u, t = torch.zeros(2, 8), torch.zeros(2), torch.ones(2)
     with pytest.raises(ValueError, match="CUDA"):

@@ -81,6 +81,7 @@ jf_status attention_call(const void* q, const void* k_cache, const void* v_cache
   if (shared != nullptr && (shared->num_groups < 0 || shared->num_groups > batch)) return JF_ERR_INVALID_ARG;
   if (batch > kMaxAttnBatch || (shared != nullptr && batch + shared->num_groups > kMaxAttnBatch))
     return JF_ERR_UNSUPPORTED;
+  if (shared != nullptr && max_pages_per_seq > kMaxSharedPages) return JF_ERR_UNSUPPORTED;
   if (static_cast<long long>(num_pages) * kPageSize >= (1ll << 31)) return JF_ERR_UNSUPPORTED;
   if (batch == 0 || total_nodes == 0) return JF_OK;
   if (!q || !k_cache || !v_cache || !block_table || !prefix_lens || !tree_offsets || !parent || !out || !workspace)

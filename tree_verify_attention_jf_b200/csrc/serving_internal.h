@@ -35,6 +35,9 @@ __host__ __device__ inline bool small_sequence(int nodes, int group, int keys) {
   return nodes * group <= kSmallRows && keys <= kSmallKeys;
 }
 
+// Block-table entries a sequence: the kernels count its slots, rounded up to a tile, in 32 bits.
+constexpr int kMaxSharedPages = (1 << 27) - 16;
+
 struct SharedAttnParams : AttnParams {
   const int32_t* group_offsets;  // [num_groups + 1] sequences
   const int32_t* shared_lens;    // [num_groups]
