@@ -84,7 +84,8 @@ typedef enum {
  *      weight that step 2 kept (1 = all of them);
  *   4. with W the weight kept, token[r] is the lowest kept id at which the running sum of the kept
  *      weights, taken in id order, exceeds u[r] * W; logprob[r] = ln(w_token / W).
- * T = 0 is greedy: the lowest id that attains m, logprob 0, whatever the other parameters are.
+ * T = 0 is greedy: the lowest id that attains m, logprob 0, whatever u[r] and the other parameters
+ * are.
  * Weights are computed in float64 (relative error below 2^-45) and summed as integers of 2^-f of the
  * row's largest (f = min(48, 62 - ceil(log2 vocab)), at least 43), so that every sum is exact and a
  * result does not depend on the order of the additions, the size of the batch or the device's
@@ -99,7 +100,8 @@ typedef enum {
  *          [rows], each may be NULL (off); token int32 [rows]; logprob float32 [rows] or NULL.
  * Limits: 1 <= vocab <= 524288, row_stride >= vocab, rows <= 2^24, logits 16-byte aligned.
  * Device checks (JF_ERR_DEVICE_CHECK; the row's outputs are left unwritten): temperature negative
- *          or not finite, top_k < 0, top_p or min_p outside [0, 1], u outside [0, 1).
+ *          or not finite; with temperature > 0 also top_k < 0, top_p or min_p outside [0, 1], u outside
+ *          [0, 1).
  * ------------------------------------------------------------------------------------------ */
 JF_API jf_status jf_sample(const void* logits, int logits_type, long long row_stride, int rows, int vocab,
                            const float* u, const float* temperature, const int32_t* top_k, const float* top_p,
@@ -126,7 +128,8 @@ JF_API jf_status jf_sample(const void* logits, int logits_type, long long row_st
  * Limits: 1 <= num_nodes <= 1024, 0 <= max_depth <= 1023, 1 <= vocab <= 524288, target_logits
  *         16-byte aligned.
  * Device checks (JF_ERR_DEVICE_CHECK; the sequence's outputs are left unwritten): parent[i] outside
- *         [-1, i-1]; the parameters as jf_sample's, and the random numbers that the walk comes to.
+ *         [-1, i-1]; the parameters as jf_sample's, and with temperature > 0 the random numbers that the
+ *         walk comes to.
  * ------------------------------------------------------------------------------------------ */
 JF_API jf_status jf_accept_sampled(const int32_t* token, const int32_t* parent, const void* target_logits,
                                    int logits_type, const float* u, const float* temperature, const int32_t* top_k,

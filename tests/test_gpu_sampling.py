@@ -203,6 +203,35 @@ def test_bad_parameters_leave_their_row_unwritten():
     check(x[11:], u[11:], [a[11:] for a in (t, k, p, m)], (tok[11:], lp[11:]))
 
 
+def test_greedy_rows_take_any_other_parameters():
+    x, rng = make_rows(16, 9, 700)
+    x[8, 3] = np.inf
+    nan, big = np.float32(np.nan), np.int32(2 ** 31 - 1)
+    u = np.array([1, -1, nan, np.inf, 0.5, 0.5, 0.5, 0.5, nan], np.float32)
+    t = np.zeros(9, np.float32)
+    t[1] = -0.0
+    k = np.array([-1, 0, -big - 1, big, -5, 1, 0, 0, -2], np.int32)
+    p = np.array([1, 2, nan, -1, np.inf, nan, 1, 0, -nan], np.float32)
+    m = np.array([0, 0, nan, 7, -1, np.inf, nan, 2, nan], np.float32)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    check(x, u, (t, k, p, m), run(x, u, (t, k, p, m), dev_status=st))
+    assert int(st.item()) == 0
+    # the same in the walk, beside a sequence that draws and one that must not be written
+    token, parent, x, _, rng = walk_case(17, 3, 40, 900, 6)
+    u = np.full((3, 7), nan, np.float32)
+    u[1] = rng.random(7, dtype=np.float32)
+    t = np.array([0, 0.5, 0.5], np.float32)
+    k, p, m = (np.array([bad, good, good], dt) for bad, good, dt in ((-3, 0, np.int32), (nan, 1, np.float32),
+                                                                     (5, 0, np.float32)))
+    out = dict(accepted_len=torch.full((3,), -9, dtype=torch.int32, device="cuda"),
+               path=torch.full((3, 7), -9, dtype=torch.int32, device="cuda"),
+               bonus=torch.full((3,), -9, dtype=torch.int32, device="cuda"), logprob=torch.full((3, 7), 3.0, device="cuda"))
+    api.accept_sampled(dev(token), dev(parent), dev(x), dev(u), dev(t), 6, dev(k), dev(p), dev(m), out=out, dev_status=st)
+    assert int(st.item()) == _lib.JF_ERR_DEVICE_CHECK and int(out["accepted_len"][2]) == -9
+    check_walk((token[:2], parent[:2], x[:2], u[:2]), [a[:2] for a in (t, k, p, m)], 6,
+               {n: v[:2] for n, v in out.items()})
+
+
 def test_repeats_graph_replays_and_streams_agree_bit_for_bit():
     x, rng = make_rows(8, 40, 50021)
     par, u = params(rng, 40, "mixed"), rng.random(40, dtype=np.float32)

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads)
   int cur = 0, L = 0, drawn = -1;
   for (int step = 0;; ++step) {
     const float us = __ldg(ub + step);  // step == L <= max_depth
-    if (!(us >= 0.f && us < 1.f)) {
+    if (!s.rp.greedy && !(us >= 0.f && us < 1.f)) {
       if (rank == 0 && tid == 0) report(status, JF_ERR_DEVICE_CHECK);
       return;  // between two draws no CTA writes into another's shared memory
     }

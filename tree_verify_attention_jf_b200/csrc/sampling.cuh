@@ -138,8 +138,9 @@ __device__ __forceinline__ RowParams read_params(const SampleParams& sp, long lo
   const float tp = sp.top_p != nullptr ? __ldg(sp.top_p + r) : 1.f;
   const float mp = sp.min_p != nullptr ? __ldg(sp.min_p + r) : 0.f;
   RowParams p;
-  p.ok = t >= 0.f && !isinf(t) && k >= 0 && tp >= 0.f && tp <= 1.f && mp >= 0.f && mp <= 1.f && u >= 0.f && u < 1.f;
-  p.greedy = t == 0.f;
+  p.greedy = t == 0.f;  // which leaves the other parameters and u out of account
+  p.ok = p.greedy || (t > 0.f && !isinf(t) && k >= 0 && tp >= 0.f && tp <= 1.f && mp >= 0.f && mp <= 1.f &&
+                      u >= 0.f && u < 1.f);
   p.t = p.greedy ? 1.0 : static_cast<double>(t);
   p.inv_t = 1.0 / p.t;
   p.ln_min_p_t = mp > 0.f ? static_cast<double>(t) * log(static_cast<double>(mp)) : -INFINITY;
