@@ -447,3 +447,49 @@ def test_walk_behind_two_to_the_31_entries():
     assert int(got["bonus"][B - 1]) == want[D][0]
     lp = got["logprob"][B - 1].cpu().numpy()
     assert all(abs(lp[i] - want[i][1]) <= LP_REL * abs(want[i][1]) + LP_ABS for i in range(D + 1))
+
+
+# Batches whose slices do not fit the shared memory that their CTAs may take, so that every pass reads the rows from
+# memory again: with one CTA a row from 149 rows on (75 for the walk) and 110 to 170 KB a row, or clusters of a few CTAs
+# for longer rows of fewer.  Odd lengths, and rows that start at every place of a 16-byte granule.
+@pytest.mark.parametrize("dtype,R,V,pad", [(torch.float32, 40, 151936, 1), (torch.float32, 80, 50003, 2),
+                                           (torch.float32, 160, 20011, 3), (torch.bfloat16, 80, 90001, 4),
+                                           (torch.bfloat16, 160, 40003, 7)])
+@pytest.mark.parametrize("kind", ["none", "top_p", "all", "mixed"])
+def test_rows_read_from_memory_in_each_pass(dtype, R, V, pad, kind):
+    x, rng = make_rows(V + R, R, V)
+    x[1, :9] = -np.inf
+    x[2, -9:] = np.nan
+    x[3] = -np.inf
+    x[4, rng.random(V) < 0.9] = -np.inf
+    x[5] = x[5].max()                            # ties throughout
+    x[6] = np.where(rng.random(V) < 0.5, np.float32(1.5), np.float32(1.25))
+    if dtype == torch.bfloat16:
+        x = bf16(x)
+    par, u = params(rng, R, kind), rng.random(R, dtype=np.float32)
+    u[0], u[-1] = 0.0, np.float32(1 - 2.0 ** -24)
+    if kind == "mixed":
+        par[1][7], par[2][7] = V // 2, 0.9       # a large top-k with a top-p
+    check(x, u, par, run(x, u, par, dtype, pad=pad))
+
+
+@pytest.mark.parametrize("dtype,B,N,V", [(torch.float32, 40, 3, 151936), (torch.float32, 80, 4, 45001),
+                                         (torch.bfloat16, 80, 4, 90001)])
+@pytest.mark.parametrize("kind", ["none", "top_p", "mixed"])
+def test_walk_over_rows_read_from_memory(dtype, B, N, V, kind):
+    case = walk_case(V + B, B, N, V, 3, lift=6.0)
+    if dtype == torch.bfloat16:
+        case = case[:2] + (bf16(case[2]),) + case[3:]
+    par = params(case[4], B, kind)
+    if kind == "mixed":
+        par[1][3], par[2][3], par[0][3] = V // 2, 0.9, 1.0
+    got = api.accept_sampled(dev(case[0]), dev(case[1]), dev(case[2], dtype), dev(case[3]), dev(par[0]), 3,
+                             *(dev(a) for a in par[1:]))
+    acc, path, bonus, lp = oracle_accept(*case[:4], 3, *par)
+    assert acc.max() > 0
+    for name, want in (("accepted_len", acc), ("path", path), ("bonus", bonus)):
+        assert np.array_equal(got[name].cpu().numpy(), want), name
+    # Each of at most V weights is off by half a step of 2^-f of the largest, so the sum, which is at least the largest,
+    # is off by V 2^-(f+1) relative, and its logarithm by as much; beside that the rounding to float32.
+    f = min(48, 62 - int(np.ceil(np.log2(V))))
+    assert (np.abs(got["logprob"].cpu().numpy() - lp) <= LP_REL * np.abs(lp) + V * 2.0 ** -(f + 1)).all()
