@@ -178,6 +178,21 @@ def test_logits_one_step_below_the_largest_at_tiny_temperatures(dtype, V):
         check(x, u, par, run(x, u, par, dtype, pad=3))
 
 
+@pytest.mark.parametrize("V", [1, 2, 100, 5000, 151936, 524288])
+def test_log_probabilities_are_never_positive(V):
+    rng = np.random.default_rng(V)
+    x = np.full((24, V), -3, np.float32)
+    x[np.arange(24), rng.integers(0, V, 24)] = 60
+    x[16:] = rng.standard_normal((8, V), dtype=np.float32)
+    k = np.where(np.arange(24) % 3 == 0, 1, 0).astype(np.int32)
+    t = np.linspace(0.1, 1.0, 24, dtype=np.float32)
+    par, u = (t, k, np.ones(24, np.float32), np.zeros(24, np.float32)), rng.random(24, dtype=np.float32)
+    tok, lp = run(x, u, par)
+    assert (lp <= 0).all()
+    alone = (k == 1) | (np.arange(24) < 16)   # e^-63 and less is below what the sums resolve: the rest weighs nothing
+    assert (lp[alone] == 0).all() and (tok[alone] == x.argmax(1)[alone]).all()
+
+
 def test_parameters_left_out_are_off():
     x, rng = make_rows(5, 4, 700)
     t, u = rng.uniform(0.5, 1, 4).astype(np.float32), rng.random(4, dtype=np.float32)

@@ -910,7 +910,9 @@ struct Row {
   }
   __device__ __forceinline__ float log_prob(float x, u64 total) const {
     const double y = (static_cast<double>(x) - md) * (c32 * (0.69314718055994530942 / kExpTab));
-    return static_cast<float>(y - (log(static_cast<double>(total)) - fx * 0.69314718055994530942));
+    // the weight kept, in units of the largest: at least 1, so that no result is above 0
+    const double kept_weight = static_cast<double>(total) * __hiloint2double((1023 - fx) << 20, 0);
+    return static_cast<float>(y - log(kept_weight));
   }
 
   // Narrows the kept set to end at its element number `k` (mass false), or at the element where the running weight
