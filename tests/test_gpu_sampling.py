@@ -465,8 +465,8 @@ def test_walk_behind_two_to_the_31_entries():
 
 
 # Batches whose slices do not fit the shared memory that their CTAs may take, so that every pass reads the rows from
-# memory again: with one CTA a row from 149 rows on (75 for the walk) and 110 to 170 KB a row, or clusters of a few CTAs
-# for longer rows of fewer.  Odd lengths, and rows that start at every place of a 16-byte granule.
+# memory again: one CTA a row from 149 rows on and about 70 KB a row, or clusters of a few CTAs for longer rows of fewer.
+# Odd lengths, and rows that start at every place of a 16-byte granule.
 @pytest.mark.parametrize("dtype,R,V,pad", [(torch.float32, 40, 151936, 1), (torch.float32, 80, 50003, 2),
                                            (torch.float32, 160, 20011, 3), (torch.bfloat16, 80, 90001, 4),
                                            (torch.bfloat16, 160, 40003, 7)])
@@ -488,10 +488,11 @@ def test_rows_read_from_memory_in_each_pass(dtype, R, V, pad, kind):
     check(x, u, par, run(x, u, par, dtype, pad=pad))
 
 
+# More sequences than the SMs hold clusters of the width that keeps a row in shared memory.
 @pytest.mark.parametrize("dtype,B,N,V", [(torch.float32, 40, 3, 151936), (torch.float32, 80, 4, 45001),
-                                         (torch.bfloat16, 80, 4, 90001)])
+                                         (torch.bfloat16, 80, 4, 90001), (torch.float32, 12, 3, 524288)])
 @pytest.mark.parametrize("kind", ["none", "top_p", "mixed"])
-def test_walk_over_rows_read_from_memory(dtype, B, N, V, kind):
+def test_walk_of_many_sequences_over_long_rows(dtype, B, N, V, kind):
     case = walk_case(V + B, B, N, V, 3, lift=6.0)
     if dtype == torch.bfloat16:
         case = case[:2] + (bf16(case[2]),) + case[3:]

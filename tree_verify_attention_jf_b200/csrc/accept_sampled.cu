@@ -20,7 +20,7 @@ constexpr int kAhead = 8;  // a tree's nodes rarely have more children than the 
 constexpr size_t kTreeOff = kSliceOff;
 constexpr size_t kWalkSliceOff = (kTreeOff + sizeof(Tree) + 127) & ~size_t(127);
 
-template <typename T, bool kResident>
+template <typename T>
 __global__ void __launch_bounds__(kThreads)
     accept_sampled_kernel(const int32_t* __restrict__ token, const int32_t* __restrict__ parent,
                           const T* __restrict__ logits, const float* __restrict__ u, const SampleParams sp,
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads)
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const long long b = blockIdx.x / C;
   const int tid = threadIdx.x;
-  Row<T, kResident> row(s, raw + kWalkSliceOff, rank, C, vocab);
+  Row<T, true> row(s, raw + kWalkSliceOff, rank, C, vocab);
   cluster.sync();  // every CTA of the cluster runs (remote shared memory may be written); the barrier is initialised
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel before this one has completed
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -106,25 +106,31 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-template <typename T, bool kResident>
+template <typename T>
 cudaError_t launch_walk(int cluster, size_t smem, const int32_t* token, const int32_t* parent, const T* logits,
                         const float* u, const SampleParams& sp, int batch, int num_nodes, int vocab, int max_depth,
                         int32_t* accepted_len, int32_t* path, int32_t* bonus, float* logprob, int32_t* status,
                         cudaStream_t stream) {
   static std::atomic<bool> done[kMaxDevices];
-  const cudaError_t e = prepare_kernel(accept_sampled_kernel<T, kResident>, done);
+  const cudaError_t e = prepare_kernel(accept_sampled_kernel<T>, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cluster;
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
-  return launch_pdl(accept_sampled_kernel<T, kResident>, dim3(static_cast<unsigned>(batch) * cluster), dim3(kThreads),
-                    smem, stream, &attr, token, parent, logits, u, sp, num_nodes, vocab, max_depth, accepted_len, path,
-                    bonus, logprob, status);
+  return launch_pdl(accept_sampled_kernel<T>, dim3(static_cast<unsigned>(batch) * cluster), dim3(kThreads), smem, stream,
+                    &attr, token, parent, logits, u, sp, num_nodes, vocab, max_depth, accepted_len, path, bonus,
+                    logprob, status);
 }
 
-// The slices stay in shared memory where they fit.
+// The cluster is as wide as its row's slices need to fit shared memory, if that is wider than the rule for all
+// sequences at once: clusters then wait for SMs, which costs less than reading rows from memory in every pass of a draw.
+// Measured on 151936 float32 entries with top-p, four steps (us; slices in shared memory / one narrow cluster a sequence
+// and rows read from memory): 38 sequences 224 / 444, 74: 342 / 478, 150: 556 / 932, 300: 1030 / 1560; the same on 80
+// rows of 45001 entries 166 / 279, of 524288 1305 / 4624.
+static_assert(kWalkSliceOff + slice_bytes(kMaxSampleVocab, kMaxCluster, sizeof(float)) <= kMaxDynSmem,
+              "the widest cluster holds any row");
 template <typename T>
 cudaError_t choose_walk(const int32_t* token, const int32_t* parent, const T* logits, const float* u,
                         const SampleParams& sp, int batch, int num_nodes, int vocab, int max_depth,
@@ -132,13 +138,10 @@ cudaError_t choose_walk(const int32_t* token, const int32_t* parent, const T* lo
                         cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const int c = widest_cluster(batch, vocab, sms);
-  const size_t smem = kWalkSliceOff + slice_bytes(vocab, c, sizeof(T));
-  if (smem <= kMaxDynSmem)
-    return launch_walk<T, true>(c, smem, token, parent, logits, u, sp, batch, num_nodes, vocab, max_depth, accepted_len,
-                                path, bonus, logprob, status, stream);
-  return launch_walk<T, false>(c, kWalkSliceOff, token, parent, logits, u, sp, batch, num_nodes, vocab, max_depth,
-                               accepted_len, path, bonus, logprob, status, stream);
+  int c = widest_cluster(batch, vocab, sms);
+  while (kWalkSliceOff + slice_bytes(vocab, c, sizeof(T)) > kMaxDynSmem) c *= 2;
+  return launch_walk<T>(c, kWalkSliceOff + slice_bytes(vocab, c, sizeof(T)), token, parent, logits, u, sp, batch,
+                        num_nodes, vocab, max_depth, accepted_len, path, bonus, logprob, status, stream);
 }
 
 }  // namespace smp

@@ -87,8 +87,8 @@ constexpr int kMinSlice = 1024;  // entries per CTA below which a wider cluster 
 constexpr size_t kTwoPerSm = 112 * 1024;  // of each of two CTAs on an SM
 
 // entries per CTA: a multiple of 8, so that a 16-byte granule belongs to one CTA when rows are aligned
-__host__ __device__ inline int slice_len(int vocab, int cluster) { return ((vocab + cluster - 1) / cluster + 7) & ~7; }
-__host__ __device__ inline size_t slice_bytes(int vocab, int cluster, int esize) {
+__host__ __device__ constexpr int slice_len(int vocab, int cluster) { return ((vocab + cluster - 1) / cluster + 7) & ~7; }
+__host__ __device__ constexpr size_t slice_bytes(int vocab, int cluster, int esize) {
   return (static_cast<size_t>(slice_len(vocab, cluster)) * esize + 32 + 127) & ~size_t(127);
 }
 
