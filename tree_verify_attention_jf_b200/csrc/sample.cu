@@ -3,9 +3,8 @@
 // Design: a thread-block cluster takes a row.  While few rows are asked for, its CTAs hold the row in shared memory, so
 // that each pass of the draw (sampling.cuh) is short; with many rows the barriers of wide clusters would dominate, and
 // narrow clusters, down to one CTA a row, read the row again from L2 in each pass.  Measured on rows of 151936 float32
-// entries with top-p alone (us; held in shared memory / read from memory, with the number of CTAs): 8 rows 31 (8) / 37
-// (16); 32 rows 46 (4) / 55 (8); 64 rows 123 (8) / 87 (4); 128 rows 227 (8) / 147 (2); 256 rows - / 273 (2), 278 (1).
-// Without filters, read from memory: 256 rows 108 (2) / 105 (1); 512 rows 183 (2) / 201 (1).
+// entries with top-p alone (us; held in shared memory / read from memory, with the number of CTAs): 8 rows 33 (8) / 39
+// (16); 32 rows 48 (4) / 58 (8); 64 rows 91 (4), 127 (8) / 90 (4); 128 rows 166 (4) / 151 (2).
 #include "sampling.cuh"
 
 namespace jf {
@@ -68,7 +67,13 @@ cudaError_t choose(const T* logits, long long row_stride, int rows, int vocab, c
   const size_t smem = kSliceOff + slice_bytes(vocab, c, sizeof(T));
   if (smem <= (rows * static_cast<long long>(c) <= sms ? kMaxDynSmem : kTwoPerSm))
     return launch<T, true>(c, smem, logits, row_stride, rows, vocab, u, sp, token, logprob, status, stream);
-  // slices that do not fit: two CTAs an SM
+  // Slices that do not fit: two CTAs an SM, and one CTA a row where two would be more than that.  Whether one is right
+  // there depends on the filters, which lie on the device: a small top-k is a chain of dependent phases that a second CTA
+  // only delays, while passes over the weights gain from it as long as SMs are left with a single row.  Small top-k with
+  // top-p and min-p, no filter, top-p, mixed filters (us, one CTA a row / two), 150 float32 rows of 66001 entries: 48 / 54,
+  // 48 / 45, 130 / 93, 129 / 92; 222 of them: 51 / 64, 50 / 47, 136 / 137, 148 / 120; 222 of 151936: 103 / 112, 105 / 86,
+  // 276 / 260, 276 / 195; no filter and top-p, 256 of 151936: 107 / 109, 280 / 276; 512: 202 / 183, 501 / 487; 1024:
+  // 344 / 352, 906 / 889.
   while (c < kMaxCluster && rows * 2ll * c <= 2 * sms && slice_len(vocab, c) > kMinSlice) c *= 2;
   return launch<T, false>(c, kSliceOff, logits, row_stride, rows, vocab, u, sp, token, logprob, status, stream);
 }

@@ -105,8 +105,9 @@ inline int sm_count() {
 }
 
 // The widest cluster with which all rows (or sequences) run at once on an SM a CTA, while a slice keeps kMinSlice
-// entries.  Clusters of 16 fill most of a GPC and wait for room once there are more than a few (8 walks of 11 steps:
-// 318 us with 16 CTAs each, 267 us with 8; one walk of 6 steps: 58 and 65 us).
+// entries.  Clusters of 16 fill most of a GPC and wait for room once there are more than a few (8 walks of 11 steps over
+// float32 rows of 151936 entries: 223 us with 16 CTAs each and 133 with 8 under a small top-k, top-p and min-p, 236 and
+// 237 under top-p alone; one walk of 6 steps: 62 and 70 us).
 inline int widest_cluster(long long rows, int vocab, int sms) {
   int c = 1;
   while (c < kMaxCluster && rows * 2 * c <= (c < 8 ? sms : sms / 2) && slice_len(vocab, c) > kMinSlice) c *= 2;
