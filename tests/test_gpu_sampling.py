@@ -509,3 +509,47 @@ def test_walk_of_many_sequences_over_long_rows(dtype, B, N, V, kind):
     # is off by V 2^-(f+1) relative, and its logarithm by as much; beside that the rounding to float32.
     f = min(48, 62 - int(np.ceil(np.log2(V))))
     assert (np.abs(got["logprob"].cpu().numpy() - lp) <= LP_REL * np.abs(lp) + V * 2.0 ** -(f + 1)).all()
+
+
+def test_waits_that_run_out_report_timeout_and_write_nothing():
+    # the debug build leaves out the copies of the rows and gives up after 50 ms; nothing faults and the next call works
+    L = _lib.debug_lib()
+    R, V, N, D = 3, 5000, 4, 2
+    x, rng = make_rows(50, R, V)
+    par, u = params(rng, R, "all"), rng.random(R, dtype=np.float32)
+    rows, st = dev(x), torch.zeros(1, dtype=torch.int32, device="cuda")
+    p = [dev(a) for a in par]
+    ptr = lambda *ts: [t.data_ptr() for t in ts]
+    token = torch.full((R,), -77, dtype=torch.int32, device="cuda")
+    lp, du = torch.full((R,), 5.0, device="cuda"), dev(u)
+    case = walk_case(51, 2, N, V, D)
+    w = [dev(a) for a in case[:4]]
+    i32 = lambda *s: torch.full(s, -9, dtype=torch.int32, device="cuda")
+    acc, path, bonus, wlp = i32(2), i32(2, D + 1), i32(2), torch.full((2, D + 1), 3.0, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def sample():
+        assert L.jf_sample(*ptr(rows), 0, V, R, V, *ptr(du, *p, token, lp, st), stream) == _lib.JF_OK
+        torch.cuda.synchronize()
+
+    def walk():
+        assert L.jf_accept_sampled(*ptr(*w[:3]), 0, *ptr(w[3], *p), 2, N, V, D, *ptr(acc, path, bonus, wlp, st),
+                                   stream) == _lib.JF_OK
+        torch.cuda.synchronize()
+
+    for call in (sample, walk):
+        st.zero_()
+        assert L.jf_debug_hold(1) == _lib.JF_OK
+        try:
+            call()
+        finally:
+            assert L.jf_debug_hold(0) == _lib.JF_OK
+        assert int(st.item()) == _lib.JF_ERR_TIMEOUT
+    assert (token == -77).all() and (lp == 5.0).all()
+    assert all((t == -9).all() for t in (acc, path, bonus)) and (wlp == 3.0).all()
+    st.zero_()
+    sample()
+    walk()
+    assert int(st.item()) == 0
+    check(x, u, par, (token.cpu().numpy(), lp.cpu().numpy()))
+    check_walk(case, [a[:2] for a in par], D, dict(accepted_len=acc, path=path, bonus=bonus, logprob=wlp))

@@ -152,6 +152,10 @@ cudaError_t choose_walk(const int32_t* token, const int32_t* parent, const T* lo
 
 }  // namespace smp
 
+#ifdef JF_DEBUG
+cudaError_t hold_accept_sampled(int on) { return cudaMemcpyToSymbol(smp::g_hold, &on, sizeof(on)); }
+#endif
+
 cudaError_t launch_accept_sampled(const int32_t* token, const int32_t* parent, const void* logits, bool bf16,
                                   const float* u, const SampleParams& sp, int batch, int num_nodes, int vocab,
                                   int max_depth, int32_t* accepted_len, int32_t* path, int32_t* bonus, float* logprob,

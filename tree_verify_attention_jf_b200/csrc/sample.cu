@@ -80,6 +80,10 @@ cudaError_t choose(const T* logits, long long row_stride, int rows, int vocab, c
 
 }  // namespace smp
 
+#ifdef JF_DEBUG
+cudaError_t hold_sample(int on) { return cudaMemcpyToSymbol(smp::g_hold, &on, sizeof(on)); }
+#endif
+
 cudaError_t launch_sample(const void* logits, bool bf16, long long row_stride, int rows, int vocab, const float* u,
                           const SampleParams& sp, int32_t* token, float* logprob, int32_t* status,
                           cudaStream_t stream) {

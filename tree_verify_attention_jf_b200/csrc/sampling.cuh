@@ -31,6 +31,12 @@
 namespace jf {
 namespace smp {
 
+#ifdef JF_DEBUG
+// Debug build only: while nonzero, a CTA announces the copy of its slice to its barrier but does not issue it, so that
+// the wait for it runs out (set by jf_debug_hold; one in each translation unit).
+static __device__ int g_hold;
+#endif
+
 namespace cg = cooperative_groups;
 using u64 = unsigned long long;
 
@@ -442,7 +448,11 @@ struct Row {
     const int full = lo < hi ? (hi - id0) / kPer : 0;
     if (tid == 0) {
       mbar_arrive_expect_tx(&s.bar, full * 16);
-      if (full > 0)
+      bool issue = full > 0;
+#ifdef JF_DEBUG
+      issue = issue && *reinterpret_cast<volatile int*>(&g_hold) == 0;
+#endif
+      if (issue)
         asm volatile(
             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                 smem_u32(buf)),

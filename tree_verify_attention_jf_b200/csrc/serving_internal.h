@@ -26,6 +26,11 @@ cudaError_t launch_accept_sampled(const int32_t* token, const int32_t* parent, c
                                   int max_depth, int32_t* accepted_len, int32_t* path, int32_t* bonus, float* logprob,
                                   int32_t* status, cudaStream_t stream);
 
+#ifdef JF_DEBUG
+cudaError_t hold_sample(int on);  // whether the kernels leave out the copies that they wait for (jf_debug_hold)
+cudaError_t hold_accept_sampled(int on);
+#endif
+
 // ---- tree attention over a shared prefix
 enum RowState : int { kRowBad = 0, kRowWhole = 1, kRowSplit = 2, kRowShares = 4 };
 

@@ -1446,6 +1446,7 @@ cudaError_t launch_tree_attention_shared(const CUtensorMap& tm_q, const CUtensor
 #ifdef JF_DEBUG
 extern "C" JF_API jf_status jf_debug_hold(int on) {
   const int v = on ? 1 : 0;
+  if (jf::hold_sample(v) != cudaSuccess || jf::hold_accept_sampled(v) != cudaSuccess) return JF_ERR_CUDA;
   return cudaMemcpyToSymbol(jf::g_debug_hold, &v, sizeof(v)) == cudaSuccess ? JF_OK : JF_ERR_CUDA;
 }
 #endif
