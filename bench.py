@@ -53,14 +53,14 @@ ROPE_THETA = 1.0e6  # rotary base of the tree K/V append timed beside the step
 DEFAULT_WORKLOAD = "qwen3_30b_a3b"
 # Kernel sources whose hash gates the recorded DRAM traffic below.
 ATTN_SOURCES = ("tree_verify_attention_jf_b200/csrc/tree_attention.cu", "tree_verify_attention_jf_b200/csrc/jf_device.cuh",
-                "tree_verify_attention_jf_b200/csrc/jf_internal.h")
+                "tree_verify_attention_jf_b200/csrc/jf_internal.h", "tree_verify_attention_jf_b200/csrc/serving_internal.h")
 # DRAM traffic of one tree_attention_kernel launch per workload (dram__bytes_read.sum + dram__bytes_write.sum of an
 # ncu capture of that workload), valid only for the kernel sources it was taken on: the roofline reports null once
 # any of them has changed.  Keys: bench workloads and legs.
 ATTN_TRAFFIC = {
-    "qwen3_30b_a3b": dict(bytes=330_625_024 + 20_950_272, source_sha256="ab96533196f3bf176fb23fda2347ab7c1c53f6f75d5a2e05f10402c5cd6803ac"),
-    "qwen3_8b": dict(bytes=20_043_776 + 34_560, source_sha256="ab96533196f3bf176fb23fda2347ab7c1c53f6f75d5a2e05f10402c5cd6803ac"),
-    "serving": dict(bytes=298_684_160 + 19_258_112, source_sha256="ab96533196f3bf176fb23fda2347ab7c1c53f6f75d5a2e05f10402c5cd6803ac"),
+    "qwen3_30b_a3b": dict(bytes=329_268_480 + 20_743_168, source_sha256="8e08d817b249bb6a8e741b9ddae5f8a4ae86cafd45a6f9ee4ad4bc9d3e475069"),
+    "qwen3_8b": dict(bytes=20_045_824 + 16_896, source_sha256="8e08d817b249bb6a8e741b9ddae5f8a4ae86cafd45a6f9ee4ad4bc9d3e475069"),
+    "serving": dict(bytes=298_688_256 + 16_867_840, source_sha256="8e08d817b249bb6a8e741b9ddae5f8a4ae86cafd45a6f9ee4ad4bc9d3e475069"),
 }
 
 

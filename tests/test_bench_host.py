@@ -79,3 +79,18 @@ def test_clock_sampler_without_a_gpu(tmp_path):
     s = bench.NvmlSampler("GPU-00000000-0000-0000-0000-000000000000", str(tmp_path / "c.csv"))
     r = s.stop()
     assert "sm_mhz" in r and "reasons" in r
+
+
+def test_the_traffic_guard_hashes_every_header_that_the_attention_kernel_includes():
+    csrc = os.path.join(bench.ROOT, "tree_verify_attention_jf_b200", "csrc")
+    seen, todo = set(), [os.path.join(csrc, "tree_attention.cu")]
+    while todo:
+        path = todo.pop()
+        seen.add(os.path.relpath(path, bench.ROOT))
+        for line in open(path):
+            if line.startswith('#include "'):
+                inc = os.path.normpath(os.path.join(os.path.dirname(path), line.split('"')[1]))
+                # the public headers hold declarations and comments only
+                if inc.startswith(csrc) and os.path.relpath(inc, bench.ROOT) not in seen:
+                    todo.append(inc)
+    assert seen == set(bench.ATTN_SOURCES)
