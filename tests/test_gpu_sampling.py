@@ -240,8 +240,10 @@ def test_greedy_rows_take_any_other_parameters():
                                                                      (5, 0, np.float32)))
     out = dict(accepted_len=torch.full((3,), -9, dtype=torch.int32, device="cuda"),
                path=torch.full((3, 7), -9, dtype=torch.int32, device="cuda"),
-               bonus=torch.full((3,), -9, dtype=torch.int32, device="cuda"), logprob=torch.full((3, 7), 3.0, device="cuda"))
-    api.accept_sampled(dev(token), dev(parent), dev(x), dev(u), dev(t), 6, dev(k), dev(p), dev(m), out=out, dev_status=st)
+               bonus=torch.full((3,), -9, dtype=torch.int32, device="cuda"),
+               logprob=torch.full((3, 7), 3.0, device="cuda"))
+    api.accept_sampled(dev(token), dev(parent), dev(x), dev(u), dev(t), 6, dev(k), dev(p), dev(m), out=out,
+                       dev_status=st)
     assert int(st.item()) == _lib.JF_ERR_DEVICE_CHECK and int(out["accepted_len"][2]) == -9
     check_walk((token[:2], parent[:2], x[:2], u[:2]), [a[:2] for a in (t, k, p, m)], 6,
                {n: v[:2] for n, v in out.items()})
@@ -465,8 +467,8 @@ def test_walk_behind_two_to_the_31_entries():
 
 
 # Batches whose slices do not fit the shared memory that their CTAs may take, so that every pass reads the rows from
-# memory again: one CTA a row from 149 rows on and about 70 KB a row, or clusters of a few CTAs for longer rows of fewer.
-# Odd lengths, and rows that start at every place of a 16-byte granule.
+# memory again: one CTA a row from 149 rows on and about 70 KB a row, or clusters of a few CTAs for longer rows of
+# fewer.  Odd lengths, and rows that start at every place of a 16-byte granule.
 @pytest.mark.parametrize("dtype,R,V,pad", [(torch.float32, 40, 151936, 1), (torch.float32, 80, 50003, 2),
                                            (torch.float32, 160, 20011, 3), (torch.bfloat16, 80, 90001, 4),
                                            (torch.bfloat16, 160, 40003, 7)])

@@ -57,8 +57,8 @@ def right(x, m, T, fx):
     return abs(weight(x, m, T, fx) - want) <= 0.5 + 2.0 ** -45 * want
 
 
-CASES = [(10.0, 1e-9), (1e4, 1e-6), (1e10, 1.0), (-3e38, 3.4e29), (2.0, 2e-9), (0.0, 1e-38), (1e-30, 1e-38), (3e38, 1e30),
-         (-5.0, 0.7), (12.0, 50.0)]
+CASES = [(10.0, 1e-9), (1e4, 1e-6), (1e10, 1.0), (-3e38, 3.4e29), (2.0, 2e-9), (0.0, 1e-38), (1e-30, 1e-38),
+         (3e38, 1e30), (-5.0, 0.7), (12.0, 50.0)]
 
 
 @pytest.mark.parametrize("fx", [43, 45, 48])

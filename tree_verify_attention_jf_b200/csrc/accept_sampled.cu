@@ -125,16 +125,16 @@ cudaError_t launch_walk(int cluster, size_t smem, const int32_t* token, const in
   attr.val.clusterDim.z = 1;
   const size_t rows_ahead = kAheadBytes / (static_cast<size_t>(batch) * vocab * sizeof(T));
   const int ahead = static_cast<int>(rows_ahead < kAhead ? rows_ahead : kAhead);
-  return launch_pdl(accept_sampled_kernel<T>, dim3(static_cast<unsigned>(batch) * cluster), dim3(kThreads), smem, stream,
-                    &attr, token, parent, logits, u, sp, num_nodes, vocab, max_depth, ahead, accepted_len, path,
-                    bonus, logprob, status);
+  return launch_pdl(accept_sampled_kernel<T>, dim3(static_cast<unsigned>(batch) * cluster), dim3(kThreads), smem,
+                    stream, &attr, token, parent, logits, u, sp, num_nodes, vocab, max_depth, ahead, accepted_len,
+                    path, bonus, logprob, status);
 }
 
 // The cluster is as wide as its row's slices need to fit shared memory, if that is wider than the rule for all
-// sequences at once: clusters then wait for SMs, which costs less than reading rows from memory in every pass of a draw.
-// Measured on 151936 float32 entries with top-p, four steps (us; slices in shared memory / one narrow cluster a sequence
-// and rows read from memory): 38 sequences 224 / 444, 74: 342 / 478, 150: 556 / 932, 300: 1030 / 1560; the same on 80
-// rows of 45001 entries 166 / 279, of 524288 1305 / 4624.
+// sequences at once: clusters then wait for SMs, which costs less than reading rows from memory in every pass of a
+// draw.  Measured on 151936 float32 entries with top-p, four steps (us; slices in shared memory / one narrow cluster a
+// sequence and rows read from memory): 38 sequences 224 / 444, 74: 342 / 478, 150: 556 / 932, 300: 1030 / 1560; 80
+// sequences with rows of 45001 entries 166 / 279, of 524288 1305 / 4624.
 static_assert(kWalkSliceOff + slice_bytes(kMaxSampleVocab, kMaxCluster, sizeof(float)) <= kMaxDynSmem,
               "the widest cluster holds any row");
 template <typename T>

@@ -68,12 +68,12 @@ cudaError_t choose(const T* logits, long long row_stride, int rows, int vocab, c
   if (smem <= (rows * static_cast<long long>(c) <= sms ? kMaxDynSmem : kTwoPerSm))
     return launch<T, true>(c, smem, logits, row_stride, rows, vocab, u, sp, token, logprob, status, stream);
   // Slices that do not fit: two CTAs an SM, and one CTA a row where two would be more than that.  Whether one is right
-  // there depends on the filters, which lie on the device: a small top-k is a chain of dependent phases that a second CTA
-  // only delays, while passes over the weights gain from it as long as SMs are left with a single row.  Small top-k with
-  // top-p and min-p, no filter, top-p, mixed filters (us, one CTA a row / two), 150 float32 rows of 66001 entries: 48 / 54,
-  // 48 / 45, 130 / 93, 129 / 92; 222 of them: 51 / 64, 50 / 47, 136 / 137, 148 / 120; 222 of 151936: 103 / 112, 105 / 86,
-  // 276 / 260, 276 / 195; no filter and top-p, 256 of 151936: 107 / 109, 280 / 276; 512: 202 / 183, 501 / 487; 1024:
-  // 344 / 352, 906 / 889.
+  // there depends on the filters, which lie on the device: a small top-k is a chain of dependent phases that a second
+  // CTA only delays, while passes over the weights gain from it as long as SMs are left with a single row.  Small top-k
+  // with top-p and min-p, no filter, top-p, mixed filters (us, one CTA a row / two), 150 float32 rows of 66001 entries:
+  // 48 / 54, 48 / 45, 130 / 93, 129 / 92; 222 of them: 51 / 64, 50 / 47, 136 / 137, 148 / 120; 222 of 151936:
+  // 103 / 112, 105 / 86, 276 / 260, 276 / 195.  No filter and top-p, 256 of 151936: 107 / 109, 280 / 276; 512:
+  // 202 / 183, 501 / 487; 1024: 344 / 352, 906 / 889.
   while (c < kMaxCluster && rows * 2ll * c <= 2 * sms && slice_len(vocab, c) > kMinSlice) c *= 2;
   return launch<T, false>(c, kSliceOff, logits, row_stride, rows, vocab, u, sp, token, logprob, status, stream);
 }

@@ -14,10 +14,10 @@
 // Weights become 64-bit integers (multiples of 2^-f of the largest): integer sums are exact, so neither atomics nor the
 // split over CTAs changes a result.
 //
-// What bounds it: with many rows the instructions of a pass over the weights, about 32 an element, 10 of them float64
-// (512 bf16 rows of 151936 entries without filters, 156 us: 75 % of the issue slots used while an SM is active, the
-// float64 pipe 35 % busy).  With few rows, latency: a barrier of the cluster takes 0.5 to 1 us, and a draw passes three
-// (small top-k) to eight of them.
+// What bounds it: with many rows the instructions of a pass over the weights (512 bf16 rows of 151936 entries without
+// filters, 156 us: 48 instructions an element, about 32 of them the weight and 10 float64; 75 % of the issue slots used
+// while an SM is active, the float64 pipe 35 % busy).  With few rows, latency: a barrier of the cluster takes 0.5 to 1
+// us, and a draw passes three (small top-k), seven (top-p alone) or about a dozen (large top-k with top-p) of them.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -93,7 +93,9 @@ constexpr int kMinSlice = 1024;  // entries per CTA below which a wider cluster 
 constexpr size_t kTwoPerSm = 112 * 1024;  // of each of two CTAs on an SM
 
 // entries per CTA: a multiple of 8, so that a 16-byte granule belongs to one CTA when rows are aligned
-__host__ __device__ constexpr int slice_len(int vocab, int cluster) { return ((vocab + cluster - 1) / cluster + 7) & ~7; }
+__host__ __device__ constexpr int slice_len(int vocab, int cluster) {
+  return ((vocab + cluster - 1) / cluster + 7) & ~7;
+}
 __host__ __device__ constexpr size_t slice_bytes(int vocab, int cluster, int esize) {
   return (static_cast<size_t>(slice_len(vocab, cluster)) * esize + 32 + 127) & ~size_t(127);
 }
@@ -111,9 +113,9 @@ inline int sm_count() {
 }
 
 // The widest cluster with which all rows (or sequences) run at once on an SM a CTA, while a slice keeps kMinSlice
-// entries.  Clusters of 16 fill most of a GPC and wait for room once there are more than a few (8 walks of 11 steps over
-// float32 rows of 151936 entries: 223 us with 16 CTAs each and 133 with 8 under a small top-k, top-p and min-p, 236 and
-// 237 under top-p alone; one walk of 6 steps: 62 and 70 us).
+// entries.  Clusters of 16 fill most of a GPC and wait for room once there are more than a few (8 walks of 11 steps
+// over float32 rows of 151936 entries: 223 us with 16 CTAs each and 133 with 8 under a small top-k, top-p and min-p,
+// 236 and 237 under top-p alone; one walk of 6 steps: 62 and 70 us).
 inline int widest_cluster(long long rows, int vocab, int sms) {
   int c = 1;
   while (c < kMaxCluster && rows * 2 * c <= (c < 8 ? sms : sms / 2) && slice_len(vocab, c) > kMinSlice) c *= 2;
